@@ -7,6 +7,10 @@ row-wise quantization covers embedding payloads. The decode half dequantizes
 and accumulates M workers' payloads in fp32 in a fixed worker order. It also
 majority-votes signSGD sign vectors.
 
+The 8-bit linear layer (``layer``) keeps activations as int8 row codes from the
+forward pass to the backward pass and multiplies from the codes; the weight
+gradients it produces are what the encode half compresses.
+
 Every step runs in hand-written CUDA kernels for sm_103a inside ``libqcodec.so``.
 The functions here only pass torch tensors' device pointers and the current
 stream through the C ABI declared in ``include/qcodec.h``, under the same names.
@@ -29,6 +33,8 @@ QC_DTYPE_F32, QC_DTYPE_BF16 = 0, 1
 QC_OUT_SUM, QC_OUT_MEAN, QC_ACCUMULATE_INTO_OUT = 0, 1, 2
 QC_MAX_WORKERS = 1024
 QC_MAX_FP8_DIM = 4096
+QC_MAX_LAYER_DIM = 1 << 20
+QC_MAX_LAYER_ROWS = 1 << 30
 QC_MAX_SEGMENTS_PER_LAUNCH = 60
 
 STATUS_NAMES = {0: "QC_OK", 1: "QC_ERR_NULL", 2: "QC_ERR_INVALID_ARG", 3: "QC_ERR_ALIGNMENT",
@@ -37,7 +43,10 @@ STATUS_NAMES = {0: "QC_OK", 1: "QC_ERR_NULL", 2: "QC_ERR_INVALID_ARG", 3: "QC_ER
 # Every symbol the C ABI exports, in header order.
 EXPORTS = ("qc_code_words", "qc_num_buckets", "qc_encode_ef", "qc_encode_ef_segments",
            "qc_decode_accumulate",
-           "qc_reencode", "qc_topk_encode_ef", "qc_topk_decode_accumulate", "qc_sign_vote", "qc_rowwise_fp8", "qc_rowwise_fp8_dequant", "qc_take_device_errors",
+           "qc_reencode", "qc_topk_encode_ef", "qc_topk_decode_accumulate", "qc_sign_vote", "qc_rowwise_fp8", "qc_rowwise_fp8_dequant",
+           "qc_rowwise_int8", "qc_rowwise_int8_dequant", "qc_int8_matmul_workspace", "qc_int8_matmul",
+           "qc_int8_input_grad_workspace", "qc_int8_input_grad", "qc_int8_weight_grad_workspace",
+           "qc_int8_weight_grad", "qc_swiglu_encode", "qc_swiglu_backward", "qc_take_device_errors",
            "qc_set_status_word", "qc_selftest_wait_timeout",
            "qc_last_error", "qc_version")
 
@@ -73,7 +82,19 @@ def _load():
     lib.qc_sign_vote.argtypes = [P, S, I, S, P, P]
     lib.qc_rowwise_fp8.argtypes = [P, S, S, P, P, P]
     lib.qc_rowwise_fp8_dequant.argtypes = [P, P, S, S, P, P]
-    for name in ("qc_encode_ef", "qc_encode_ef_segments", "qc_decode_accumulate", "qc_reencode", "qc_topk_encode_ef",
+    lib.qc_rowwise_int8.argtypes = [P, I, S, S, S, P, P, P]
+    lib.qc_rowwise_int8_dequant.argtypes = [P, P, S, S, P, I, S, P]
+    lib.qc_int8_matmul.argtypes = [P, P, P, P, P, S, S, S, P, I, S, P, S, P]
+    lib.qc_int8_input_grad.argtypes = [P, S, P, P, S, S, S, P, I, S, P, S, P]
+    lib.qc_int8_weight_grad.argtypes = [P, S, P, P, S, S, S, P, I, P, I, P, S, P]
+    lib.qc_swiglu_encode.argtypes = [P, I, S, S, S, P, P, P, P, P]
+    lib.qc_swiglu_backward.argtypes = [P, I, S, P, P, S, S, P, S, P]
+    for name in ("qc_int8_matmul_workspace", "qc_int8_input_grad_workspace",
+                 "qc_int8_weight_grad_workspace"):
+        getattr(lib, name).argtypes, getattr(lib, name).restype = [S, S, S], S
+    for name in ("qc_rowwise_int8", "qc_rowwise_int8_dequant", "qc_int8_matmul", "qc_int8_input_grad",
+                 "qc_int8_weight_grad", "qc_swiglu_encode", "qc_swiglu_backward",
+                 "qc_encode_ef", "qc_encode_ef_segments", "qc_decode_accumulate", "qc_reencode", "qc_topk_encode_ef",
                  "qc_topk_decode_accumulate", "qc_sign_vote",
                  "qc_rowwise_fp8",
                  "qc_rowwise_fp8_dequant"):
@@ -470,3 +491,11 @@ def decode_accumulate(codes, scale, offset, *, n, bits, bucket, scheme=QC_SCHEME
     qc_decode_accumulate(codes, cs, scale, offset, ms, M, n, bits, bucket, scheme, out, flags,
                          stream=stream)
     return out
+
+
+# the 8-bit linear layer (needs the names above)
+from .layer import (int8_input_grad, int8_matmul, int8_weight_grad, qc_int8_input_grad,  # noqa: E402,F401
+                    qc_int8_input_grad_workspace, qc_int8_matmul, qc_int8_matmul_workspace,
+                    qc_int8_weight_grad, qc_int8_weight_grad_workspace, qc_rowwise_int8,
+                    qc_rowwise_int8_dequant, qc_swiglu_backward, qc_swiglu_encode, rowwise_int8,
+                    rowwise_int8_dequant, swiglu_backward, swiglu_encode)

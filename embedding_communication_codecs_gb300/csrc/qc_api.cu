@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/qcodec.h"
+#include "qc_api_util.h"
 #include "qc_internal.h"
 
 static_assert(int{QC_SCHEME_UNIFORM} == qc::kUniform && int{QC_SCHEME_SIGN} == qc::kSign &&
@@ -25,6 +26,11 @@ namespace {
 thread_local char g_last_error[512] = "";
 // The status word that launches from this thread report failures into.
 thread_local uint32_t *g_status_word = nullptr;
+
+}  // namespace
+
+namespace qc {
+namespace api {
 
 qc_status fail(qc_status st, const char *fmt, ...) {
     va_list ap;
@@ -45,14 +51,18 @@ qc_status from_cuda(cudaError_t e, const char *what) {
                 cudaGetErrorString(e));
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+uint32_t *status_word() { return g_status_word; }
 
-// [a, a+na) and [b, b+nb) (bytes) share a byte.
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
+}  // namespace api
+}  // namespace qc
+
+namespace {
+
+using qc::api::aligned;
+using qc::api::fail;
+using qc::api::from_cuda;
+using qc::api::ok;
+using qc::api::overlaps;
 
 bool valid_bucket(size_t bucket) { return bucket >= 32 && bucket % 32 == 0 && bucket <= (1u << 24); }
 

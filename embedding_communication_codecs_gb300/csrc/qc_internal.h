@@ -291,6 +291,68 @@ cudaError_t launch_vote(const VoteParams &p, bool vectorised, cudaStream_t strea
 cudaError_t launch_fp8_quant(const Fp8Params &p, cudaStream_t stream);
 cudaError_t launch_fp8_dequant(const Fp8Params &p, cudaStream_t stream);
 
+// ---------------------------------------------------------------------------
+// The 8-bit linear layer (qc_int8_rows.cu, qc_int8_product.cu).
+
+struct RowCodesParams {
+    const void *x;        // rows of fp32 or bf16
+    uint64_t x_stride;    // elements between rows
+    uint64_t rows;
+    uint32_t dim;
+    int8_t *codes;
+    float *row_scale;
+    const int8_t *codes_in;
+    const float *scale_in;
+    void *out;
+    uint64_t out_stride;
+};
+
+struct SwigluParams {
+    const void *in;       // gate_up (encode) or dh (backward)
+    uint64_t in_stride;
+    uint64_t rows;
+    uint32_t dim;
+    int8_t *h_codes;
+    float *h_scale;
+    int8_t *saved_codes;
+    float *saved_scale;
+    const int8_t *saved_codes_in;
+    const float *saved_scale_in;
+    void *dgate_up;
+    uint64_t dgate_up_stride;
+};
+
+cudaError_t launch_rows_int8_encode(const RowCodesParams &p, int bf16, cudaStream_t stream);
+cudaError_t launch_rows_int8_decode(const RowCodesParams &p, int bf16, cudaStream_t stream);
+cudaError_t launch_swiglu_encode(const SwigluParams &p, int bf16, cudaStream_t stream);
+cudaError_t launch_swiglu_backward(const SwigluParams &p, int bf16, cudaStream_t stream);
+
+// One product of the layer: out[M, N] = sum over L of the operands named per launcher.
+struct ProductParams {
+    const int8_t *x_codes;
+    const float *x_scale;
+    const int8_t *w_codes;
+    const float *w_scale;
+    const float *bias;
+    const uint16_t *dy;
+    uint64_t dy_stride;
+    uint64_t T, N, K;
+    void *out;
+    int out_bf16;
+    uint64_t out_stride;
+    float *dbias;
+    int accumulate;
+    uint32_t *status;
+    void *workspace;
+};
+
+size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K);
+size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K);
+size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K);
+cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream);
+cudaError_t launch_int8_input_grad(const ProductParams &p, cudaStream_t stream);
+cudaError_t launch_int8_weight_grad(const ProductParams &p, cudaStream_t stream);
+
 // Persistent grid: min(work units, SMs x resident blocks of `kernel` with
 // `smem` bytes of dynamic shared memory).
 int persistent_grid(const void *kernel, int block, uint64_t units, size_t smem = 0);

@@ -1,0 +1,347 @@
+"""The 8-bit linear layer: activations kept as int8 row codes from the forward
+pass to the backward pass, the products that read those codes, and the gated
+activation between two layers.
+
+The ``qc_`` functions carry the C ABI's names and arguments (``include/qcodec.h``
+states the arithmetic).  The functions without the prefix take tensors only: they
+read the sizes from the shapes, allocate the results and the workspace on the
+stream they run on, and return the results.
+
+    x_codes, x_scale = rowwise_int8(x)                    # [T, K], kept for the backward pass
+    y = int8_matmul(x_codes, x_scale, w_codes, w_scale)   # [T, N]
+    dx = int8_input_grad(dy, w_codes, w_scale)            # [T, K]
+    dw, _ = int8_weight_grad(dy, x_codes, x_scale)        # [N, K], flat for encode_ef
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import (QC_ACCUMULATE_INTO_OUT, QC_DTYPE_BF16, QC_DTYPE_F32, _check, _need, _on_device, _ptr,
+               _stream, lib)
+
+_I8 = (torch.int8,)
+_F32 = (torch.float32,)
+_BF16 = (torch.bfloat16,)
+_CODE_OF = {torch.float32: QC_DTYPE_F32, torch.bfloat16: QC_DTYPE_BF16}
+_TYPE_OF = {QC_DTYPE_F32: _F32, QC_DTYPE_BF16: _BF16}
+
+
+def _span(rows, dim, stride, esize):
+    return ((rows - 1) * stride + dim) * esize if rows else 0
+
+
+def _matrix(t, name, rows, dim, stride, dtype):
+    """A strided matrix argument of the C ABI: type, dense rows, span."""
+    if dtype not in _TYPE_OF:
+        return  # the library refuses it
+    _need(t, name, _span(rows, dim, stride, 4 if dtype == QC_DTYPE_F32 else 2), _TYPE_OF[dtype], flat=False)
+    if rows > 1 and t is not None and not isinstance(t, int) and t.dim() == 2 and t.stride(0) != stride:
+        raise ValueError(f"{name}'s row stride ({t.stride(0)}) differs from the stride passed ({stride})")
+
+
+# ----------------------------------------------------------------- the C ABI
+
+def qc_rowwise_int8(x, dtype, x_stride, rows, dim, codes, row_scale, stream=None):
+    """Rows of fp32 or bf16 -> int8 codes and one power-of-two scale per row."""
+    if rows:
+        _matrix(x, "x", rows, dim, x_stride, dtype)
+        _need(codes, "codes", rows * dim, _I8)
+        _need(row_scale, "row_scale", 4 * rows, _F32)
+        _on_device(x=x, codes=codes, row_scale=row_scale)
+    _check(lib.qc_rowwise_int8(_ptr(x), dtype, x_stride, rows, dim, _ptr(codes), _ptr(row_scale),
+                               _stream(stream)))
+
+
+def qc_rowwise_int8_dequant(codes, row_scale, rows, dim, out, out_dtype, out_stride, stream=None):
+    """Row codes -> fp32 or bf16 rows."""
+    if rows:
+        _need(codes, "codes", rows * dim, _I8)
+        _need(row_scale, "row_scale", 4 * rows, _F32)
+        _matrix(out, "out", rows, dim, out_stride, out_dtype)
+        _on_device(codes=codes, row_scale=row_scale, out=out)
+    _check(lib.qc_rowwise_int8_dequant(_ptr(codes), _ptr(row_scale), rows, dim, _ptr(out), out_dtype,
+                                       out_stride, _stream(stream)))
+
+
+def qc_int8_matmul_workspace(T, N, K) -> int:
+    """Bytes of workspace that qc_int8_matmul needs."""
+    return int(lib.qc_int8_matmul_workspace(T, N, K))
+
+
+def qc_int8_input_grad_workspace(T, N, K) -> int:
+    """Bytes of workspace that qc_int8_input_grad needs."""
+    return int(lib.qc_int8_input_grad_workspace(T, N, K))
+
+
+def qc_int8_weight_grad_workspace(T, N, K) -> int:
+    """Bytes of workspace that qc_int8_weight_grad needs."""
+    return int(lib.qc_int8_weight_grad_workspace(T, N, K))
+
+
+def qc_int8_matmul(x_codes, x_scale, w_codes, w_scale, bias, T, N, K, y, y_dtype, y_stride, workspace,
+                   workspace_bytes, stream=None):
+    """y = (x_codes w_codes^T) with a scale per token and per output channel, plus bias."""
+    if T:
+        _need(x_codes, "x_codes", T * K, _I8)
+        _need(x_scale, "x_scale", 4 * T, _F32)
+        _need(w_codes, "w_codes", N * K, _I8)
+        _need(w_scale, "w_scale", 4 * N, _F32)
+        _need(bias, "bias", 4 * N, _F32)
+        _matrix(y, "y", T, N, y_stride, y_dtype)
+        _need(workspace, "workspace", workspace_bytes)
+        _on_device(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias, y=y,
+                   workspace=workspace)
+    _check(lib.qc_int8_matmul(_ptr(x_codes), _ptr(x_scale), _ptr(w_codes), _ptr(w_scale), _ptr(bias), T, N,
+                              K, _ptr(y), y_dtype, y_stride, _ptr(workspace), workspace_bytes,
+                              _stream(stream)))
+
+
+def qc_int8_input_grad(dy, dy_stride, w_codes, w_scale, T, N, K, dx, dx_dtype, dx_stride, workspace,
+                       workspace_bytes, stream=None):
+    """dx = dy (w_codes * w_scale)."""
+    if T:
+        _matrix(dy, "dy", T, N, dy_stride, QC_DTYPE_BF16)
+        _need(w_codes, "w_codes", N * K, _I8)
+        _need(w_scale, "w_scale", 4 * N, _F32)
+        _matrix(dx, "dx", T, K, dx_stride, dx_dtype)
+        _need(workspace, "workspace", workspace_bytes)
+        _on_device(dy=dy, w_codes=w_codes, w_scale=w_scale, dx=dx, workspace=workspace)
+    _check(lib.qc_int8_input_grad(_ptr(dy), dy_stride, _ptr(w_codes), _ptr(w_scale), T, N, K, _ptr(dx),
+                                  dx_dtype, dx_stride, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def qc_int8_weight_grad(dy, dy_stride, x_codes, x_scale, T, N, K, dw, dw_dtype, dbias, flags, workspace,
+                        workspace_bytes, stream=None):
+    """dw = dy^T (x_codes * x_scale), dbias = column sums of dy (dbias may be None)."""
+    if T:
+        _matrix(dy, "dy", T, N, dy_stride, QC_DTYPE_BF16)
+        _need(x_codes, "x_codes", T * K, _I8)
+        _need(x_scale, "x_scale", 4 * T, _F32)
+    if dw_dtype in _TYPE_OF:
+        _need(dw, "dw", N * K * (4 if dw_dtype == QC_DTYPE_F32 else 2), _TYPE_OF[dw_dtype])
+    _need(dbias, "dbias", 4 * N, _F32)
+    _need(workspace, "workspace", workspace_bytes)
+    _on_device(dy=dy, x_codes=x_codes, x_scale=x_scale, dw=dw, dbias=dbias, workspace=workspace)
+    _check(lib.qc_int8_weight_grad(_ptr(dy), dy_stride, _ptr(x_codes), _ptr(x_scale), T, N, K, _ptr(dw),
+                                   dw_dtype, _ptr(dbias), flags, _ptr(workspace), workspace_bytes,
+                                   _stream(stream)))
+
+
+def qc_swiglu_encode(gate_up, dtype, stride, rows, dim, h_codes, h_scale, saved_codes, saved_scale,
+                     stream=None):
+    """h = silu(gate) * up as row codes, and the row codes of gate and up."""
+    if rows:
+        _matrix(gate_up, "gate_up", rows, 2 * dim, stride, dtype)
+        _need(h_codes, "h_codes", rows * dim, _I8)
+        _need(h_scale, "h_scale", 4 * rows, _F32)
+        _need(saved_codes, "saved_codes", 2 * rows * dim, _I8)
+        _need(saved_scale, "saved_scale", 8 * rows, _F32)
+        _on_device(gate_up=gate_up, h_codes=h_codes, h_scale=h_scale, saved_codes=saved_codes,
+                   saved_scale=saved_scale)
+    _check(lib.qc_swiglu_encode(_ptr(gate_up), dtype, stride, rows, dim, _ptr(h_codes), _ptr(h_scale),
+                                _ptr(saved_codes), _ptr(saved_scale), _stream(stream)))
+
+
+def qc_swiglu_backward(dh, dtype, dh_stride, saved_codes, saved_scale, rows, dim, dgate_up,
+                       dgate_up_stride, stream=None):
+    """The gradients by gate and up, from their row codes."""
+    if rows:
+        _matrix(dh, "dh", rows, dim, dh_stride, dtype)
+        _need(saved_codes, "saved_codes", 2 * rows * dim, _I8)
+        _need(saved_scale, "saved_scale", 8 * rows, _F32)
+        _matrix(dgate_up, "dgate_up", rows, 2 * dim, dgate_up_stride, dtype)
+        _on_device(dh=dh, saved_codes=saved_codes, saved_scale=saved_scale, dgate_up=dgate_up)
+    _check(lib.qc_swiglu_backward(_ptr(dh), dtype, dh_stride, _ptr(saved_codes), _ptr(saved_scale), rows,
+                                  dim, _ptr(dgate_up), dgate_up_stride, _stream(stream)))
+
+
+# -------------------------------------------------------------- conveniences
+
+def _rows(t, name, dtypes, shape=None):
+    """A matrix whose rows are dense: its shape is checked, its row stride returned."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}; expected one of {dtypes}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {shape}")
+    r, d = t.shape
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be dense along its last dimension")
+    stride = t.stride(0) if r > 1 else d
+    if stride < d:
+        raise ValueError(f"{name}'s rows overlap (row stride {stride}, row length {d})")
+    return stride
+
+
+def _dense(t, name, dtypes, shape):
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a tensor of shape {shape} and dtype {dtypes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _codes(codes, scale, what):
+    """Row codes and their scales: the shape of the matrix they stand for."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+        raise ValueError(f"{what}_codes must be a 2-D tensor")
+    shape = tuple(codes.shape)
+    _dense(codes, f"{what}_codes", _I8, shape)
+    _dense(scale, f"{what}_scale", _F32, (shape[0],))
+    return shape
+
+
+def _dtype(dtype):
+    if dtype not in _CODE_OF:
+        raise ValueError(f"dtype {dtype} is not torch.float32 or torch.bfloat16")
+    return _CODE_OF[dtype]
+
+
+def _on(stream):
+    """Results and workspaces belong to the stream that the call runs on, so that the
+    allocator reuses their memory in that stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _scratch(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def rowwise_int8(x, *, stream=None):
+    """int8 codes of x's shape and one fp32 power-of-two scale per row.
+
+    ``x`` is [rows, dim] fp32 or bf16 with dense rows."""
+    stride = _rows(x, "x", (torch.float32, torch.bfloat16))
+    _on_device(x=x)
+    rows, dim = x.shape
+    with _on(stream):
+        codes = torch.empty((rows, dim), dtype=torch.int8, device=x.device)
+        scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        _check(lib.qc_rowwise_int8(x.data_ptr(), _CODE_OF[x.dtype], stride, rows, dim, codes.data_ptr(),
+                                   scale.data_ptr(), _stream(stream)))
+    return codes, scale
+
+
+def rowwise_int8_dequant(codes, row_scale, *, dtype=torch.bfloat16, stream=None):
+    """The rows that the codes stand for."""
+    rows, dim = _codes(codes, row_scale, "row")
+    code = _dtype(dtype)
+    _on_device(codes=codes, row_scale=row_scale)
+    with _on(stream):
+        out = torch.empty((rows, dim), dtype=dtype, device=codes.device)
+        _check(lib.qc_rowwise_int8_dequant(codes.data_ptr(), row_scale.data_ptr(), rows, dim,
+                                           out.data_ptr(), code, dim, _stream(stream)))
+    return out
+
+
+def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bfloat16, stream=None):
+    """y [T, N] from the codes of x [T, K] and of w [N, K], their scales, and an
+    optional fp32 bias [N]."""
+    T, K = _codes(x_codes, x_scale, "x")
+    N, kw = _codes(w_codes, w_scale, "w")
+    if kw != K:
+        raise ValueError(f"w_codes has rows of {kw}, x_codes of {K}")
+    if bias is not None:
+        _dense(bias, "bias", _F32, (N,))
+    code = _dtype(dtype)
+    _on_device(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias)
+    with _on(stream):
+        y = torch.empty((T, N), dtype=dtype, device=x_codes.device)
+        nbytes = lib.qc_int8_matmul_workspace(T, N, K)
+        ws = _scratch(nbytes, x_codes.device)
+        _check(lib.qc_int8_matmul(x_codes.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
+                                  w_scale.data_ptr(), _ptr(bias), T, N, K, y.data_ptr(), code, N,
+                                  _ptr(ws), nbytes, _stream(stream)))
+    return y
+
+
+def int8_input_grad(dy, w_codes, w_scale, *, dtype=torch.bfloat16, stream=None):
+    """dx [T, K] from dy [T, N] bf16 (dense rows) and the codes of w [N, K]."""
+    N, K = _codes(w_codes, w_scale, "w")
+    stride = _rows(dy, "dy", _BF16)
+    T = dy.shape[0]
+    if dy.shape[1] != N:
+        raise ValueError(f"dy has rows of {dy.shape[1]}, w_codes has {N} rows")
+    code = _dtype(dtype)
+    _on_device(dy=dy, w_codes=w_codes, w_scale=w_scale)
+    with _on(stream):
+        dx = torch.empty((T, K), dtype=dtype, device=dy.device)
+        nbytes = lib.qc_int8_input_grad_workspace(T, N, K)
+        ws = _scratch(nbytes, dy.device)
+        _check(lib.qc_int8_input_grad(dy.data_ptr(), stride, w_codes.data_ptr(), w_scale.data_ptr(), T, N,
+                                      K, dx.data_ptr(), code, K, _ptr(ws), nbytes, _stream(stream)))
+    return dx
+
+
+def int8_weight_grad(dy, x_codes, x_scale, *, dtype=torch.float32, with_bias=False, into=None,
+                     stream=None):
+    """(dw [N, K], dbias [N] fp32 or None) from dy [T, N] bf16 (dense rows) and the
+    codes of x [T, K].  ``into`` = (dw, dbias or None), fp32: the gradients are
+    added to them and they are returned."""
+    T, K = _codes(x_codes, x_scale, "x")
+    stride = _rows(dy, "dy", _BF16)
+    N = dy.shape[1]
+    if dy.shape[0] != T:
+        raise ValueError(f"dy has {dy.shape[0]} rows, x_codes {T}")
+    if into is not None:
+        dw, dbias = into
+        _dense(dw, "dw", _F32, (N, K))
+        if dbias is not None:
+            _dense(dbias, "dbias", _F32, (N,))
+        _on_device(dw=dw, dbias=dbias)
+        dtype = torch.float32
+    code = _dtype(dtype)
+    _on_device(dy=dy, x_codes=x_codes, x_scale=x_scale)
+    with _on(stream):
+        if into is None:
+            dw = torch.empty((N, K), dtype=dtype, device=dy.device)
+            dbias = torch.empty((N,), dtype=torch.float32, device=dy.device) if with_bias else None
+        nbytes = lib.qc_int8_weight_grad_workspace(T, N, K)
+        ws = _scratch(nbytes, dy.device)
+        _check(lib.qc_int8_weight_grad(dy.data_ptr(), stride, x_codes.data_ptr(), x_scale.data_ptr(), T, N,
+                                       K, dw.data_ptr(), code, _ptr(dbias),
+                                       0 if into is None else QC_ACCUMULATE_INTO_OUT, _ptr(ws), nbytes,
+                                       _stream(stream)))
+    return dw, dbias
+
+
+def swiglu_encode(gate_up, *, stream=None):
+    """(h_codes [T, F], h_scale [T], saved_codes [T, 2F], saved_scale [T, 2]) of
+    gate_up [T, 2F], a row's F gates followed by its F ups (dense rows, fp32 or bf16)."""
+    stride = _rows(gate_up, "gate_up", (torch.float32, torch.bfloat16))
+    rows, two = gate_up.shape
+    if two % 2:
+        raise ValueError(f"gate_up has rows of {two}; an even number is needed")
+    dim, dev = two // 2, gate_up.device
+    _on_device(gate_up=gate_up)
+    with _on(stream):
+        h_codes = torch.empty((rows, dim), dtype=torch.int8, device=dev)
+        h_scale = torch.empty((rows,), dtype=torch.float32, device=dev)
+        saved_codes = torch.empty((rows, two), dtype=torch.int8, device=dev)
+        saved_scale = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+        _check(lib.qc_swiglu_encode(gate_up.data_ptr(), _CODE_OF[gate_up.dtype], stride, rows, dim,
+                                    h_codes.data_ptr(), h_scale.data_ptr(), saved_codes.data_ptr(),
+                                    saved_scale.data_ptr(), _stream(stream)))
+    return h_codes, h_scale, saved_codes, saved_scale
+
+
+def swiglu_backward(dh, saved_codes, saved_scale, *, stream=None):
+    """dgate_up [T, 2F] of dh's type from dh [T, F] (dense rows, fp32 or bf16) and
+    what swiglu_encode saved."""
+    stride = _rows(dh, "dh", (torch.float32, torch.bfloat16))
+    rows, dim = dh.shape
+    _dense(saved_codes, "saved_codes", _I8, (rows, 2 * dim))
+    _dense(saved_scale, "saved_scale", _F32, (rows, 2))
+    _on_device(dh=dh, saved_codes=saved_codes, saved_scale=saved_scale)
+    with _on(stream):
+        out = torch.empty((rows, 2 * dim), dtype=dh.dtype, device=dh.device)
+        _check(lib.qc_swiglu_backward(dh.data_ptr(), _CODE_OF[dh.dtype], stride, saved_codes.data_ptr(),
+                                      saved_scale.data_ptr(), rows, dim, out.data_ptr(), 2 * dim,
+                                      _stream(stream)))
+    return out

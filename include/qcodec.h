@@ -381,6 +381,113 @@ qc_status qc_rowwise_fp8(const float *x, size_t rows, size_t dim, uint8_t *codes
 qc_status qc_rowwise_fp8_dequant(const uint8_t *codes, const float *row_scale, size_t rows,
                                  size_t dim, float *out, qc_stream_t stream);
 
+/* ======================================================================== *
+ * The 8-bit linear layer: activations kept as int8 codes from the forward
+ * pass to the backward pass, the products that read those codes, and the gated
+ * activation between two layers.
+ *
+ * Row codes.  A row x of a matrix is held as int8 codes c and one fp32 scale s,
+ * x_j ~ c_j * s, where s is the smallest power of two from 2^-126 to 2^121 with
+ * max|x| / s < 127.5 and c_j = rint(x_j / s), ties to even, so |c_j| <= 127.
+ * (Above 127.5 * 2^121 there is none: s = 2^121, and codes saturate at 127.)
+ * A power of two makes every c_j * s exact in bf16, which the backward products
+ * multiply on the tensor cores; it costs at most one of the eight bits (half a
+ * bit on average) against s = max|x| / 127.  A row of zeros has s = 0 and codes
+ * 0.  A row that holds a NaN or an infinity has s = NaN and codes 0: it decodes
+ * to NaN, so a bad step stays visible in every result that reads the row.
+ *
+ * Matrices are row-major.  "stride" is the distance between rows in elements;
+ * codes and scales are dense.  T (tokens) or rows may be 0; N, K and dim are
+ * 1 .. QC_MAX_LAYER_DIM, T and rows up to QC_MAX_LAYER_ROWS, a matrix up to 2^40
+ * elements.  Buffers need the alignment of their elements; a call is faster
+ * where rows start on 16-byte boundaries.  Outputs must not overlap inputs.
+ *
+ * Workspace: the products take scratch memory of at least the bytes that the
+ * matching _workspace function gives for the same sizes (it may be 0), 256-byte
+ * aligned, not shared with another call in flight.  Its contents before the call
+ * do not matter and nothing in it lasts.
+ * ======================================================================== */
+#define QC_MAX_LAYER_DIM (1 << 20)
+#define QC_MAX_LAYER_ROWS (1 << 30)
+
+/*
+ * qc_rowwise_int8 -- rows of fp32 or bf16 -> row codes as above.
+ * x : rows x dim, stride x_stride >= dim.  codes : rows x dim.  row_scale : rows.
+ */
+qc_status qc_rowwise_int8(const void *x, qc_dtype dtype, size_t x_stride, size_t rows, size_t dim,
+                          int8_t *codes, float *row_scale, qc_stream_t stream);
+
+/*
+ * qc_rowwise_int8_dequant -- out_rj = codes_rj * row_scale_r, rounded to the
+ * output's type (exact for the scales of qc_rowwise_int8).
+ */
+qc_status qc_rowwise_int8_dequant(const int8_t *codes, const float *row_scale, size_t rows,
+                                  size_t dim, void *out, qc_dtype out_dtype, size_t out_stride,
+                                  qc_stream_t stream);
+
+/*
+ * qc_int8_matmul -- y_tn = (sum_k x_codes_tk * w_codes_nk) * (x_scale_t * w_scale_n) + bias_n
+ * for any int8 codes and fp32 scales (one per token, one per output channel).
+ * The sum is held in fp32 and is exact while its partial sums stay below 2^24.
+ * x_codes : T x K.  w_codes : N x K.  bias : N fp32, or NULL.  y : T x N fp32 or bf16.
+ */
+size_t qc_int8_matmul_workspace(size_t T, size_t N, size_t K);
+qc_status qc_int8_matmul(const int8_t *x_codes, const float *x_scale, const int8_t *w_codes,
+                         const float *w_scale, const float *bias, size_t T, size_t N, size_t K,
+                         void *y, qc_dtype y_dtype, size_t y_stride, void *workspace,
+                         size_t workspace_bytes, qc_stream_t stream);
+
+/*
+ * qc_int8_input_grad -- the gradient by the layer's input:
+ *   dx_tk = sum_n dy_tn * (w_codes_nk * w_scale_n), summed in fp32.
+ * The decoded weight is a bf16: exact for the scales of qc_rowwise_int8, rounded
+ * once for others.  dy : T x N bf16.  dx : T x K fp32 or bf16.
+ */
+size_t qc_int8_input_grad_workspace(size_t T, size_t N, size_t K);
+qc_status qc_int8_input_grad(const void *dy, size_t dy_stride, const int8_t *w_codes,
+                             const float *w_scale, size_t T, size_t N, size_t K, void *dx,
+                             qc_dtype dx_dtype, size_t dx_stride, void *workspace,
+                             size_t workspace_bytes, qc_stream_t stream);
+
+/*
+ * qc_int8_weight_grad -- the gradients by the layer's weights and bias, from the
+ * codes that the forward pass read:
+ *   dw_nk = sum_t dy_tn * (x_codes_tk * x_scale_t),   dbias_n = sum_t dy_tn,
+ * summed in fp32; the decoded activation is a bf16 as above.
+ * dy : T x N bf16.  dw : N x K fp32 or bf16, dense (a flat gradient, as
+ * qc_encode_ef takes it).  dbias : N fp32, or NULL.
+ * flags : 0, or QC_ACCUMULATE_INTO_OUT to add to what dw and dbias hold (dw then
+ * fp32).  With T == 0 the gradients are zero.
+ */
+size_t qc_int8_weight_grad_workspace(size_t T, size_t N, size_t K);
+qc_status qc_int8_weight_grad(const void *dy, size_t dy_stride, const int8_t *x_codes,
+                              const float *x_scale, size_t T, size_t N, size_t K, void *dw,
+                              qc_dtype dw_dtype, float *dbias, int flags, void *workspace,
+                              size_t workspace_bytes, qc_stream_t stream);
+
+/*
+ * qc_swiglu_encode -- the gated activation between two layers, kept in 8 bits.
+ * gate_up : rows x (2 dim), a row's dim gates followed by its dim ups, fp32 or
+ * bf16.  h_j = gate_j / (1 + exp(-gate_j)) * up_j in fp32 becomes the row codes
+ * (h_codes, h_scale) that the next layer's qc_int8_matmul and qc_int8_weight_grad
+ * read.  saved_codes : rows x (2 dim), the row codes of gate and of up, each with
+ * a scale of its own in saved_scale : rows x 2.
+ */
+qc_status qc_swiglu_encode(const void *gate_up, qc_dtype dtype, size_t stride, size_t rows,
+                           size_t dim, int8_t *h_codes, float *h_scale, int8_t *saved_codes,
+                           float *saved_scale, qc_stream_t stream);
+
+/*
+ * qc_swiglu_backward -- from the decoded g and u, with sig = 1 / (1 + exp(-g)):
+ *   dgate_j = dh_j * u_j * sig_j * (1 + g_j * (1 - sig_j)),   dup_j = dh_j * g_j * sig_j
+ * in fp32, rounded once.  dh : rows x dim.  dgate_up : rows x (2 dim), laid out as
+ * gate_up.  dh and dgate_up have the same type, fp32 or bf16.
+ */
+qc_status qc_swiglu_backward(const void *dh, qc_dtype dtype, size_t dh_stride,
+                             const int8_t *saved_codes, const float *saved_scale, size_t rows,
+                             size_t dim, void *dgate_up, size_t dgate_up_stride,
+                             qc_stream_t stream);
+
 /*
  * qc_take_device_errors -- device-side failures of the pipelined kernels.
  *
