@@ -1,96 +1,339 @@
-// qc_int8_product.cu -- the products of the 8-bit linear layer.
+// qc_int8_product.cu -- the products of the 8-bit linear layer on the tensor cores.
 //
-// out[m, n] = sum over l of A(m, l) * B(l, n), both operands read as fp32 through
-// a functor and summed in order of l by one thread per output, in 64 x 64 tiles.
+// sm_103a has no 8-bit integer matrix instruction, so the codes are widened to bf16
+// (exactly: |code| <= 128 times a power of two) and every product is
+//
+//     out[m, n] = sum over l of A(m, l) B(n, l),   bf16 x bf16 -> fp32,
+//
+// with each operand either K-major (rows of the outer index) or MN-major (rows of
+// the contraction index), as it lies in memory:
+//
+//     matmul       A = x codes [T, K]   K-major    B = w codes [N, K]   K-major
+//     input grad   A = dy      [T, N]   K-major    B = w values [N, K]  MN-major
+//     weight grad  A = dy      [T, N]   MN-major   B = x values [T, K]  MN-major
+//
+// A pair of blocks (a cluster of two) owns a 256 x BN tile: each holds 128 rows of A
+// and BN / 2 rows of B per step of 64 along l, and 128 x BN sums in its tensor
+// memory, twice, so that one tile is stored while the next is summed.  Warp 0 loads
+// (TMA), warp 1 of the leading block issues the matrix instructions, warps 2 to 5
+// store.  Every wait is bounded (qc_pipeline.cuh).
+#include <cuda.h>
+
+#include <mutex>
+
 #include "qc_int8_rows.cuh"
 #include "qc_internal.h"
+#include "qc_tc.cuh"
 
 namespace qc {
+
+__device__ unsigned int g_product_error;
+QC_DEFINE_TAKE_FLAG(take_product_errors, g_product_error)
+
 namespace {
 
-constexpr int kTile = 64, kDepth = 16, kThreads = 256;
+constexpr int kStep = 64;       // contraction elements per stage: one 128-byte row
+constexpr int kBlockM = 128;    // rows of A per block
+constexpr int kPairM = 2 * kBlockM;
+constexpr int kGemmThreads = 192;
+constexpr int kGroupM = 8;      // tiles along M that share their B tiles in L2
 
-struct Shape {
-    uint64_t M, N, L;
+template <int BN>
+struct Tile {
+    static constexpr int kRowsB = BN / 2;
+    static constexpr int kBytesA = kBlockM * kStep * 2, kBytesB = kRowsB * kStep * 2;
+    static constexpr int kStage = kBytesA + kBytesB;
+    static constexpr int kStages = BN == 256 ? 6 : 8;
+    static constexpr int kTmemCols = 2 * BN;
+    static constexpr int kSmem = kStages * kStage + 1024;  // tiles start on 1024 bytes
 };
 
-// A and B: float operator()(outer index, l).  Out: void operator()(m, n, sum).
-template <typename A, typename B, typename Out>
-__global__ void __launch_bounds__(kThreads) product(const Shape S, const A a, const B b, const Out out) {
-    __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-    const uint64_t ntn = (S.N + kTile - 1) / kTile;
-    const uint64_t m0 = blockIdx.x / ntn * kTile, n0 = blockIdx.x % ntn * kTile;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float acc[4][4] = {};
-    for (uint64_t l0 = 0; l0 < S.L; l0 += kDepth) {
-        for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-            const int r = i / kDepth, l = i % kDepth;
-            const bool in = l0 + l < S.L;
-            sa[l][r] = in && m0 + r < S.M ? a(m0 + r, l0 + l) : 0.0f;
-            sb[l][r] = in && n0 + r < S.N ? b(n0 + r, l0 + l) : 0.0f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int l = 0; l < kDepth; ++l)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __fmaf_rn(sa[l][ty + 16 * i], sb[l][tx + 16 * j], acc[i][j]);
-        __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < S.M && n < S.N) out(m, n, acc[i][j]);
-        }
+struct GemmParams {
+    uint64_t M, N, L;
+    void *out;
+    uint64_t out_stride;
+    int out_bf16, accumulate, vector_out;
+    const float *m_scale, *n_scale, *bias;
+    uint32_t *status;
+};
+
+// Tile t of the grid of 256 x BN tiles: groups of kGroupM tile rows, column by column
+// inside a group.
+__device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t &m, uint32_t &n) {
+    const uint32_t per_group = kGroupM * tiles_n;
+    const uint32_t g = t / per_group, r = t % per_group;
+    const uint32_t rows = min(tiles_m - g * kGroupM, static_cast<uint32_t>(kGroupM));
+    m = g * kGroupM + r % rows;
+    n = r / rows;
 }
 
-struct CodeRows {  // (row, l) of dense codes
-    const int8_t *codes;
-    uint64_t dim;
-    __device__ float operator()(uint64_t r, uint64_t l) const { return codes[r * dim + l]; }
-};
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 
-struct DecodedColumns {  // (column, l) of decoded codes, rounded to bf16; l is the row
-    const int8_t *codes;
-    const float *scale;
-    uint64_t dim;
-    __device__ float operator()(uint64_t c, uint64_t l) const {
-        return bf16_bits_to_float(to_bf16(__fmul_rn(codes[l * dim + c], scale[l])));
+// 32 sums of row m from column n on: scale, bias, store.
+__device__ __forceinline__ void store_chunk(const GemmParams &P, uint64_t m, uint64_t n, const uint32_t (&acc)[32]) {
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(acc[j]);
+    const bool whole = n + 32 <= P.N;
+    if (P.m_scale) {
+        const float ms = __ldg(P.m_scale + m);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (whole || n + j < P.N) v[j] = __fmul_rn(v[j], __fmul_rn(ms, __ldg(P.n_scale + n + j)));
     }
-};
-
-struct Bf16Rows {
-    const uint16_t *x;
-    uint64_t stride;
-    __device__ float operator()(uint64_t r, uint64_t l) const { return bf16_bits_to_float(x[r * stride + l]); }
-};
-
-struct Bf16Columns {
-    const uint16_t *x;
-    uint64_t stride;
-    __device__ float operator()(uint64_t c, uint64_t l) const { return bf16_bits_to_float(x[l * stride + c]); }
-};
-
-struct StoreOut {
-    void *out;
-    uint64_t stride;
-    int bf16, accumulate;
-    const float *m_scale, *n_scale, *bias;
-    __device__ void operator()(uint64_t m, uint64_t n, float v) const {
-        if (m_scale) v = __fmul_rn(v, __fmul_rn(m_scale[m], n_scale[n]));
-        if (bias) v = __fadd_rn(v, bias[n]);
-        if (bf16) {
-            static_cast<uint16_t *>(out)[m * stride + n] = to_bf16(v);
+    if (P.bias) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (whole || n + j < P.N) v[j] = __fadd_rn(v[j], __ldg(P.bias + n + j));
+    }
+    if (P.out_bf16) {
+        uint16_t *o = static_cast<uint16_t *>(P.out) + m * P.out_stride + n;
+        if (whole && P.vector_out) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+                *reinterpret_cast<uint4 *>(o + j) = make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
+                                                               pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
         } else {
-            float *o = static_cast<float *>(out) + m * stride + n;
-            *o = accumulate ? __fadd_rn(*o, v) : v;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (n + j < P.N) o[j] = to_bf16(v[j]);
+        }
+    } else {
+        float *o = static_cast<float *>(P.out) + m * P.out_stride + n;
+        if (whole && P.vector_out) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                if (P.accumulate) {
+                    const float4 c = *reinterpret_cast<const float4 *>(o + j);
+                    w = make_float4(__fadd_rn(c.x, w.x), __fadd_rn(c.y, w.y), __fadd_rn(c.z, w.z), __fadd_rn(c.w, w.w));
+                }
+                *reinterpret_cast<float4 *>(o + j) = w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (n + j < P.N) o[j] = P.accumulate ? __fadd_rn(o[j], v[j]) : v[j];
         }
     }
+}
+
+template <int BN, bool A_MN, bool B_MN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmParams P) {
+    using T = Tile<BN>;
+    constexpr int S = T::kStages;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t full[S], empty[S], sums_full[2], sums_empty[2], drained;
+    __shared__ uint32_t tmem_slot;
+    uint8_t *const tiles = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const uint32_t tiles_m = static_cast<uint32_t>((P.M + kPairM - 1) / kPairM);
+    const uint32_t tiles_n = static_cast<uint32_t>((P.N + BN - 1) / BN);
+    const uint32_t ntiles = tiles_m * tiles_n, npairs = gridDim.x / 2, pair = blockIdx.x / 2;
+    const uint32_t steps = static_cast<uint32_t>((P.L + kStep - 1) / kStep);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);     // the leading block's load thread; bytes of both blocks
+            mbar_init(&empty[s], 1);    // the matrix instructions that read the stage
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sums_full[b], 1);
+            mbar_init(&sums_empty[b], 8);  // four storing warps in each block
+        }
+        mbar_init(&drained, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc_pair<T::kTmemCols>(&tmem_slot);
+    if (threadIdx.x == 0) {
+        prefetch_map(&map_a);
+        prefetch_map(&map_b);
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            for (uint32_t t = pair; t < ntiles && ok; t += npairs) {
+                uint32_t tm, tn;
+                tile_at(t, tiles_m, tiles_n, tm, tn);
+                const int m0 = static_cast<int>(tm * kPairM + rank * kBlockM);
+                const int n0 = static_cast<int>(tn * BN + rank * T::kRowsB);
+                for (uint32_t k = 0; k < steps; ++k, ++it) {
+                    const uint32_t s = it % S, phase = (it / S) & 1;
+                    if (!mbar_wait_cluster(&empty[s], phase ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = in_block(&full[s], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * T::kStage);
+                    uint8_t *a = tiles + s * T::kStage, *b = a + T::kBytesA;
+                    const int l0 = static_cast<int>(k * kStep);
+                    if (A_MN) {
+                        tma_load_pair(a, &map_a, m0, l0, bar);
+                        tma_load_pair(a + T::kBytesA / 2, &map_a, m0 + 64, l0, bar);
+                    } else {
+                        tma_load_pair(a, &map_a, l0, m0, bar);
+                    }
+                    if (B_MN) {
+#pragma unroll
+                        for (int j = 0; j < T::kRowsB / 64; ++j)
+                            tma_load_pair(b + j * 64 * kStep * 2, &map_b, n0 + 64 * j, l0, bar);
+                    } else {
+                        tma_load_pair(b, &map_b, l0, n0, bar);
+                    }
+                }
+            }
+            // no block leaves while a copy into either one is in flight
+            if (rank == 0)
+                for (uint32_t i = it > S ? it - S : 0; i < it; ++i) ok &= mbar_wait_cluster(&full[i % S], (i / S) & 1);
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t kInstr = bf16_instruction(kPairM, BN, A_MN, B_MN);
+            // 16 contraction elements on: 32 bytes inside a row, or 16 rows of 128 bytes
+            constexpr uint32_t kNextA = (A_MN ? 2048 : 32) >> 4, kNextB = (B_MN ? 2048 : 32) >> 4;
+            uint32_t it = 0, i = 0;
+            for (uint32_t t = pair; t < ntiles && ok; t += npairs, ++i) {
+                const uint32_t buf = i & 1;
+                if (!mbar_wait_cluster(&sums_empty[buf], ((i >> 1) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (uint32_t k = 0; k < steps; ++k, ++it) {
+                    const uint32_t s = it % S;
+                    if (!mbar_wait_cluster(&full[s], (it / S) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a = smem_operand(tiles + s * T::kStage, 64 * kStep * 2);
+                    const uint64_t b = smem_operand(tiles + s * T::kStage + T::kBytesA, 64 * kStep * 2);
+#pragma unroll
+                    for (int j = 0; j < kStep / 16; ++j)
+                        mma_pair(tmem + buf * BN, a + j * kNextA, b + j * kNextB, kInstr, (k | j) != 0);
+                    mma_commit_pair(&empty[s]);
+                }
+                mma_commit_pair(&sums_full[buf]);
+            }
+            mma_commit_pair(&drained);
+        }
+        // neither block leaves before the leading block's last instruction and the
+        // arrivals that it sent to both blocks
+        if (lane == 0) ok &= mbar_wait_cluster(&drained, 0);
+    } else {
+        const int quarter = warp & 3;  // the 32 lanes of tensor memory that this warp may read
+        uint32_t i = 0;
+        for (uint32_t t = pair; t < ntiles; t += npairs, ++i) {
+            uint32_t tm, tn;
+            tile_at(t, tiles_m, tiles_n, tm, tn);
+            const uint32_t buf = i & 1;
+            ok = mbar_wait_cluster(&sums_full[buf], (i >> 1) & 1);
+            if (__any_sync(kFull, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t m = static_cast<uint64_t>(tm) * kPairM + rank * kBlockM + quarter * 32 + lane;
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 32) {
+                const uint64_t n = static_cast<uint64_t>(tn) * BN + c;
+                if (n >= P.N) break;
+                uint32_t acc[32];
+                tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + c, acc);
+                tmem_wait_load();
+                if (m < P.M) store_chunk(P, m, n, acc);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(in_block(&sums_empty[buf], 0));
+        }
+    }
+    if (!ok) report_failure(&g_product_error, P.status, kErrPipelineTimeout);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) tmem_free_pair<T::kTmemCols>(tmem);
+}
+
+// ------------------------------------------------------------------ the host
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A matrix of 16-bit elements, `rows` rows of `dim` elements `stride` apart, as
+// boxes of box_rows x 64 under the 128-byte swizzle; zeros outside.
+bool make_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t dim, uint64_t stride, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {dim, rows}, strides[1] = {stride * 2};
+    const cuuint32_t box[2] = {64, box_rows}, unit[2] = {1, 1};
+    EncodeTiled fn = encode_tiled();
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, unit,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A 16-bit operand in memory.
+struct Operand {
+    const void *p;
+    uint64_t rows, dim, stride;
 };
+
+bool tma_fits(const void *p, uint64_t stride) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
+}
+
+template <int BN, bool A_MN, bool B_MN>
+cudaError_t launch_gemm(const Operand &a, const Operand &b, GemmParams g, cudaStream_t stream) {
+    using T = Tile<BN>;
+    const auto kernel = gemm<BN, A_MN, B_MN>;
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, a.p, a.rows, a.dim, a.stride, A_MN ? kStep : kBlockM) ||
+        !make_map(&mb, b.p, b.rows, b.dim, b.stride, B_MN ? kStep : T::kRowsB))
+        return cudaErrorInvalidValue;
+    cudaError_t e = prepare_dynamic_smem(reinterpret_cast<const void *>(kernel), T::kSmem);
+    if (e != cudaSuccess) return e;
+    const uint64_t ntiles = ((g.M + kPairM - 1) / kPairM) * ((g.N + BN - 1) / BN);
+    if (ntiles > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    const int esize = g.out_bf16 ? 2 : 4;
+    g.vector_out = (reinterpret_cast<uintptr_t>(g.out) & 15) == 0 && (g.out_stride * esize) % 16 == 0;
+    // one block per SM, in pairs
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const uint64_t pairs = ntiles < static_cast<uint64_t>(sms / 2) ? ntiles : sms / 2;
+    kernel<<<static_cast<unsigned>(2 * pairs), kGemmThreads, T::kSmem, stream>>>(ma, mb, g);
+    return cudaGetLastError();
+}
+
+template <bool A_MN, bool B_MN>
+cudaError_t launch_product(const Operand &a, const Operand &b, const GemmParams &g, cudaStream_t stream) {
+    return launch_gemm<256, A_MN, B_MN>(a, b, g, stream);
+}
 
 __global__ void column_sums(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t cols, float *out,
                             int accumulate) {
@@ -102,35 +345,100 @@ __global__ void column_sums(const uint16_t *x, uint64_t stride, uint64_t rows, u
     out[c] = accumulate ? __fadd_rn(out[c], v) : v;
 }
 
-template <typename A, typename B>
-cudaError_t launch(const Shape &s, const A &a, const B &b, const StoreOut &o, cudaStream_t stream) {
-    const uint64_t tiles = ((s.M + kTile - 1) / kTile) * ((s.N + kTile - 1) / kTile);
-    if (tiles > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
-    product<<<static_cast<unsigned>(tiles), kThreads, 0, stream>>>(s, a, b, o);
+// Rows of 16-bit elements copied to rows that TMA can read.
+__global__ void copy_rows(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t dim, uint16_t *out,
+                          uint64_t out_stride) {
+    for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (uint64_t j = threadIdx.x; j < dim; j += blockDim.x) out[r * out_stride + j] = x[r * stride + j];
+}
+
+// Row length, in elements, of a widened matrix in the workspace: whole 128-byte rows.
+uint64_t padded(uint64_t dim) { return (dim + 63) / 64 * 64; }
+uint64_t widened_bytes(uint64_t rows, uint64_t dim) { return (rows * padded(dim) * 2 + 255) / 256 * 256; }
+
+// Codes (times their scale, if there is one) as bf16 rows in the workspace.
+cudaError_t widen(const int8_t *codes, const float *scale, uint64_t rows, uint64_t dim, void *to, Operand &op,
+                  cudaStream_t stream) {
+    RowCodesParams p{};
+    p.codes_in = codes;
+    p.scale_in = scale;
+    p.rows = rows;
+    p.dim = static_cast<uint32_t>(dim);
+    p.out = to;
+    p.out_stride = padded(dim);
+    op = {to, rows, dim, padded(dim)};
+    return launch_rows_int8_decode(p, 1, stream);
+}
+
+// dy as TMA can read it: in place, or copied to the workspace.
+cudaError_t readable_dy(const ProductParams &p, void *room, Operand &op, cudaStream_t stream) {
+    op = {p.dy, p.T, p.N, p.dy_stride};
+    if (tma_fits(p.dy, p.dy_stride)) return cudaSuccess;
+    op = {room, p.T, p.N, padded(p.N)};
+    const int grid = persistent_grid(reinterpret_cast<const void *>(&copy_rows), 256, p.T);
+    copy_rows<<<grid, 256, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N, static_cast<uint16_t *>(room), padded(p.N));
     return cudaGetLastError();
+}
+
+GemmParams outputs(const ProductParams &p, uint64_t M, uint64_t N, uint64_t L) {
+    GemmParams g{};
+    g.M = M;
+    g.N = N;
+    g.L = L;
+    g.out = p.out;
+    g.out_stride = p.out_stride;
+    g.out_bf16 = p.out_bf16;
+    g.accumulate = p.accumulate;
+    g.status = p.status;
+    return g;
 }
 
 }  // namespace
 
-size_t int8_matmul_workspace(uint64_t, uint64_t, uint64_t) { return 0; }
-size_t int8_input_grad_workspace(uint64_t, uint64_t, uint64_t) { return 0; }
-size_t int8_weight_grad_workspace(uint64_t, uint64_t, uint64_t) { return 0; }
+size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K) {
+    return widened_bytes(T, K) + widened_bytes(N, K);
+}
+size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
+    return widened_bytes(N, K) + widened_bytes(T, N);
+}
+size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
+    return widened_bytes(T, K) + widened_bytes(T, N);
+}
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
-    return launch({p.T, p.N, p.K}, CodeRows{p.x_codes, p.K}, CodeRows{p.w_codes, p.K},
-                  StoreOut{p.out, p.out_stride, p.out_bf16, 0, p.x_scale, p.w_scale, p.bias}, stream);
+    Operand x, w;
+    uint8_t *ws = static_cast<uint8_t *>(p.workspace);
+    cudaError_t e = widen(p.x_codes, nullptr, p.T, p.K, ws, x, stream);
+    if (e == cudaSuccess) e = widen(p.w_codes, nullptr, p.N, p.K, ws + widened_bytes(p.T, p.K), w, stream);
+    if (e != cudaSuccess) return e;
+    GemmParams g = outputs(p, p.T, p.N, p.K);
+    g.m_scale = p.x_scale;
+    g.n_scale = p.w_scale;
+    g.bias = p.bias;
+    return launch_product<false, false>(x, w, g, stream);
 }
 
 cudaError_t launch_int8_input_grad(const ProductParams &p, cudaStream_t stream) {
-    return launch({p.T, p.K, p.N}, Bf16Rows{p.dy, p.dy_stride}, DecodedColumns{p.w_codes, p.w_scale, p.K},
-                  StoreOut{p.out, p.out_stride, p.out_bf16, 0, nullptr, nullptr, nullptr}, stream);
+    Operand dy, w;
+    uint8_t *ws = static_cast<uint8_t *>(p.workspace);
+    cudaError_t e = widen(p.w_codes, p.w_scale, p.N, p.K, ws, w, stream);
+    if (e == cudaSuccess) e = readable_dy(p, ws + widened_bytes(p.N, p.K), dy, stream);
+    if (e != cudaSuccess) return e;
+    return launch_product<false, true>(dy, w, outputs(p, p.T, p.K, p.N), stream);
 }
 
 cudaError_t launch_int8_weight_grad(const ProductParams &p, cudaStream_t stream) {
-    cudaError_t e = launch({p.N, p.K, p.T}, Bf16Columns{p.dy, p.dy_stride},
-                           DecodedColumns{p.x_codes, p.x_scale, p.K},
-                           StoreOut{p.out, p.out_stride, p.out_bf16, p.accumulate, nullptr, nullptr, nullptr},
-                           stream);
+    cudaError_t e;
+    if (p.T == 0) {  // not accumulating: the gradients are zero
+        e = cudaMemsetAsync(p.out, 0, p.N * p.K * (p.out_bf16 ? 2 : 4), stream);
+        if (e == cudaSuccess && p.dbias) e = cudaMemsetAsync(p.dbias, 0, p.N * 4, stream);
+        return e;
+    }
+    Operand dy, x;
+    uint8_t *ws = static_cast<uint8_t *>(p.workspace);
+    e = widen(p.x_codes, p.x_scale, p.T, p.K, ws, x, stream);
+    if (e == cudaSuccess) e = readable_dy(p, ws + widened_bytes(p.T, p.K), dy, stream);
+    if (e == cudaSuccess) e = launch_product<true, true>(dy, x, outputs(p, p.N, p.K, p.T), stream);
     if (e != cudaSuccess || !p.dbias) return e;
     column_sums<<<static_cast<unsigned>((p.N + 127) / 128), 128, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N,
                                                                               p.dbias, p.accumulate);

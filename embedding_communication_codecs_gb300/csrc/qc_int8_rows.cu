@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kRowThreads) rows_encode(const RowCodesParams 
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) rows_decode(const RowCodesParams P) {
     for (uint64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
-        const float s = P.scale_in[r];
+        const float s = P.scale_in ? P.scale_in[r] : 1.0f;
         T *out = static_cast<T *>(P.out) + r * P.out_stride;
         for (uint32_t j = threadIdx.x; j < P.dim; j += kRowThreads)
             store_from_float(out + j, __fmul_rn(static_cast<float>(P.codes_in[r * P.dim + j]), s));

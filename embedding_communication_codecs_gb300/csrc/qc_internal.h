@@ -302,7 +302,7 @@ struct RowCodesParams {
     int8_t *codes;
     float *row_scale;
     const int8_t *codes_in;
-    const float *scale_in;
+    const float *scale_in;  // or null: the codes themselves (decode only)
     void *out;
     uint64_t out_stride;
 };
@@ -377,6 +377,7 @@ cudaError_t take_topk_errors(uint32_t *flags);
 cudaError_t take_encode_bf16_errors(uint32_t *flags);
 cudaError_t take_encode_bf16_fast_errors(uint32_t *flags);
 cudaError_t take_decode_errors(uint32_t *flags);
+cudaError_t take_product_errors(uint32_t *flags);
 cudaError_t take_reencode_errors(uint32_t *flags);
 
 }  // namespace qc

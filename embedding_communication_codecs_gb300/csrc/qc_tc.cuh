@@ -1,0 +1,154 @@
+// qc_tc.cuh -- fifth-generation tensor core (tcgen05), tensor memory and tiled TMA
+// helpers for blocks that work in pairs (a cluster of two, cta_group::2), next to
+// the mbarrier helpers of qc_pipeline.cuh.
+#pragma once
+
+#include <cuda.h>
+
+#include "qc_pipeline.cuh"
+
+namespace qc {
+
+// ------------------------------------------------------------------ clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The address of `p` (this block's shared memory) in the block of the given rank.
+__device__ __forceinline__ uint32_t in_block(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+// ------------------------------------------------------------------ barriers
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kTryWaitHintNs)
+        : "memory");
+    return done != 0;
+}
+
+// mbar_wait() for a barrier that the other block of the pair arrives on too.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    const long long c0 = clock64();
+    for (uint32_t r = 1; r < kWaitRoundsBackstop; ++r) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (global_ns() - t0 > kWaitNs || clock64() - c0 > static_cast<long long>(4 * kWaitNs)) return false;
+    }
+    return false;
+}
+
+// Arrive on a barrier of any block of the cluster (an in_block() address).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// ----------------------------------------------------------------- tiled TMA
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// The box at (x, y) of a 2-D map into this block's shared memory; the bytes are
+// counted on the barrier at `bar`, which may be the pair's other block's.
+__device__ __forceinline__ void tma_load_pair(void *dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+// ------------------------------------------------------------- tensor memory
+
+template <int COLS>
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *slot) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
+                 "n"(COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+
+template <int COLS>
+__device__ __forceinline__ void tmem_free_pair(uint32_t tmem) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(COLS) : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 consecutive fp32 columns of the calling warp's 32 lanes.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// --------------------------------------------------------- matrix instructions
+
+// Shared-memory operand of 16-bit elements in 128-byte rows under the 128-byte
+// swizzle, in groups of eight rows (1024 bytes).  Along the rows: the contraction
+// runs inside a row for a K-major operand (row = outer index), and across rows for
+// an MN-major one (row = contraction index, 64 outer indexes a row), where
+// `mn_stride` is the distance between blocks of 64 outer indexes.
+__device__ __forceinline__ uint64_t smem_operand(const void *p, uint32_t mn_stride) {
+    return static_cast<uint64_t>((smem_u32(p) & 0x3FFFFu) >> 4) |
+           (static_cast<uint64_t>(mn_stride >> 4) << 16) |  // leading dimension offset (MN-major only)
+           (static_cast<uint64_t>(1024 >> 4) << 32) |       // stride between groups of eight rows
+           (1ull << 46) |                                   // descriptor version
+           (2ull << 61);                                    // 128-byte swizzle
+}
+
+// Instruction descriptor: bf16 x bf16 -> fp32, M x N tile, each operand K- or MN-major.
+__host__ __device__ constexpr uint32_t bf16_instruction(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+           (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+           (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// D (+)= A B for the pair of blocks, issued by one thread of the leading one.
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(instr), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// Arrive on the barrier at this offset in both blocks once this thread's earlier
+// matrix instructions are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::
+            "r"(smem_u32(bar)),
+        "h"(static_cast<unsigned short>(3))
+        : "memory");
+}
+
+}  // namespace qc
