@@ -1,8 +1,14 @@
 // qc_int8_rows.cu -- row codes of activations and back, and the gated activation
 // that keeps its inputs and its result in row codes.
 //
-// One block owns a row: a pass for the row's largest magnitude, and a pass that
-// writes the codes (the second read hits L2).
+// All four kernels move a few bytes per element and compute little: memory
+// bandwidth bounds them.  A team of 8 to 512 lanes (a power of two) owns a row and
+// covers it in units of U consecutive elements, V units per lane at a time.  The
+// encoders read a row once, hold it in registers while the team agrees on the
+// largest magnitude, and write the codes from there; a row that is longer than
+// the largest team holds is read a second time, from L2.  U is 8 (or 16) where
+// rows start on the vector's boundary, so that a lane moves 8 to 32 bytes with one
+// instruction, and 1 elsewhere.
 #include "qc_int8_rows.cuh"
 #include "qc_internal.h"
 
@@ -11,76 +17,268 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// Largest of v over the block, in every thread.
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *red) {
-    v = __reduce_max_sync(kFull, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
+// U consecutive elements of a row, as they lie in memory.
+template <int U>
+struct alignas(U * 4 > 16 ? 16 : U * 4) RawF32 {
+    float v[U];
+    __device__ __forceinline__ float get(int j) const { return v[j]; }
+};
+template <int U>
+struct alignas(U * 2 > 16 ? 16 : U * 2) RawBf16 {
+    uint16_t v[U];
+    __device__ __forceinline__ float get(int j) const { return bf16_bits_to_float(v[j]); }
+};
+template <typename T, int U>
+struct RawOf;
+template <int U>
+struct RawOf<float, U> {
+    using type = RawF32<U>;
+};
+template <int U>
+struct RawOf<uint16_t, U> {
+    using type = RawBf16<U>;
+};
+
+template <typename T, int U>
+__device__ __forceinline__ typename RawOf<T, U>::type load_unit(const T *p) {
+    return *reinterpret_cast<const typename RawOf<T, U>::type *>(p);
+}
+
+// The codes of U elements, four to a word.
+template <int U>
+__device__ __forceinline__ void store_codes(int8_t *p, const uint32_t (&c)[U]) {
+    if constexpr (U == 1) {
+        *p = static_cast<int8_t>(c[0] & 0xFFu);
+    } else {
+        static_assert(U == 8, "a unit is 8 bytes of codes");
+        *reinterpret_cast<uint2 *>(p) =
+            make_uint2(pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7]));
+    }
+}
+
+// U fp32 values rounded to the output's type.
+template <typename T, int U>
+__device__ __forceinline__ void store_values(T *p, const float (&v)[U]) {
+    typename RawOf<T, U>::type r;
 #pragma unroll
-    for (int w = 1; w < kRowThreads / 32; ++w) v = max(v, red[w]);
-    return v;
+    for (int j = 0; j < U; ++j) store_from_float(&r.v[j], v[j]);
+    *reinterpret_cast<typename RawOf<T, U>::type *>(p) = r;
 }
 
-__device__ __forceinline__ int8_t code_of(float x, const RowScale &s) {
-    if (s.inverse == 0.0f) return 0;
-    if (s.saturates) x = clamp_to_cap(x);
-    return static_cast<int8_t>(code_bits(x, s.inverse) & 0xFFu);
+// A team of `lanes` threads (a power of two, 8 to THREADS) and the rows it owns.
+struct Team {
+    uint32_t lanes, lane, first, stride;
+    __device__ explicit Team(uint32_t lanes_) : lanes(lanes_) {
+        const uint32_t teams = blockDim.x / lanes;
+        lane = threadIdx.x & (lanes - 1);
+        first = blockIdx.x * teams + threadIdx.x / lanes;
+        stride = gridDim.x * teams;
+    }
+};
+
+// The largest of v[0..N) over the team, in every lane.  A team of several warps
+// meets in shared memory, in one of two buffers used in turn, so one block barrier
+// a row is enough; every thread of the block takes part.
+template <int N>
+__device__ __forceinline__ void team_max(uint32_t (&v)[N], uint32_t lanes, uint32_t (*red)[16][N], int &turn) {
+    if (lanes >= 32) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __reduce_max_sync(kFull, v[i]);
+    } else {
+        for (uint32_t o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = max(v[i], __shfl_xor_sync(kFull, v[i], o));
+    }
+    if (lanes > 32) {
+        const uint32_t warp = threadIdx.x >> 5, w0 = threadIdx.x / lanes * (lanes >> 5);
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[turn][warp][i] = v[i];
+        __syncthreads();
+        for (uint32_t w = 0; w < (lanes >> 5); ++w)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = max(v[i], red[turn][w0 + w][i]);
+        turn ^= 1;
+    }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) rows_encode(const RowCodesParams P) {
-    __shared__ uint32_t red[kRowThreads / 32];
-    for (uint64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
+// Codes of U elements.  A row whose codes are all zero may hold infinities or NaN:
+// they are not multiplied.
+template <int U, typename Get>
+__device__ __forceinline__ void encode_unit(int8_t *out, const RowScale &s, Get get) {
+    uint32_t c[U];
+    if (s.inverse == 0.0f) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) c[j] = 0u;
+    } else if (s.saturates) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) c[j] = code_bits(clamp_to_cap(get(j)), s.inverse);
+    } else {
+#pragma unroll
+        for (int j = 0; j < U; ++j) c[j] = code_bits(get(j), s.inverse);
+    }
+    store_codes<U>(out, c);
+}
+
+template <typename T, int U, int V>
+__global__ void __launch_bounds__(kRowThreads) rows_encode(const RowCodesParams P, uint32_t lanes) {
+    __shared__ uint32_t red[2][16][1];
+    using R = typename RawOf<T, U>::type;
+    const Team team(lanes);
+    const uint32_t units = P.dim / U, chunk = lanes * V;
+    int turn = 0;
+    // every team of the block goes round as often as the block's first one
+    for (uint64_t r0 = team.first - threadIdx.x / lanes; r0 < P.rows; r0 += team.stride) {
+        const uint64_t r = r0 + threadIdx.x / lanes;
+        const bool live = r < P.rows;
         const T *x = static_cast<const T *>(P.x) + r * P.x_stride;
-        uint32_t m = 0;
-        for (uint32_t j = threadIdx.x; j < P.dim; j += kRowThreads) m = max(m, abs_bits(load_as_float(x + j)));
-        const RowScale s = row_scale_of(block_max(m, red));
-        for (uint32_t j = threadIdx.x; j < P.dim; j += kRowThreads)
-            P.codes[r * P.dim + j] = code_of(load_as_float(x + j), s);
-        if (threadIdx.x == 0) P.row_scale[r] = s.scale;
+        R held[V];
+        uint32_t m[1] = {0};
+        for (uint32_t base = 0; base < units; base += chunk) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t u = base + v * lanes + team.lane;
+                if (live && u < units) held[v] = load_unit<T, U>(x + static_cast<uint64_t>(u) * U);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t u = base + v * lanes + team.lane;
+                if (live && u < units)
+#pragma unroll
+                    for (int j = 0; j < U; ++j) m[0] = max(m[0], abs_bits(held[v].get(j)));
+            }
+        }
+        team_max(m, lanes, red, turn);
+        const RowScale s = row_scale_of(m[0]);
+        if (!live) continue;
+        int8_t *out = P.codes + r * P.dim;
+        for (uint32_t base = 0; base < units; base += chunk) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t u = base + v * lanes + team.lane;
+                if (u < units) {
+                    const R h = units <= chunk ? held[v] : load_unit<T, U>(x + static_cast<uint64_t>(u) * U);
+                    encode_unit<U>(out + static_cast<uint64_t>(u) * U, s, [&](int j) { return h.get(j); });
+                }
+            }
+        }
+        if (team.lane == 0) P.row_scale[r] = s.scale;
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) rows_decode(const RowCodesParams P) {
-    for (uint64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
-        const float s = P.scale_in ? P.scale_in[r] : 1.0f;
+// U codes as they lie in memory.  A code becomes a float without a conversion
+// instruction (those run at a quarter of the rate): its byte, offset by 128, under
+// the exponent of 2^23, minus 2^23 + 128.
+template <int U>
+struct alignas(U) RawCodes {
+    uint32_t w[U / 4];
+    __device__ __forceinline__ float get(int j) const {
+        return __fsub_rn(__uint_as_float(__byte_perm(w[j / 4] ^ 0x80808080u, 0x4B000000u, 0x7440 + (j & 3))), 8388736.0f);
+    }
+};
+template <>
+struct RawCodes<1> {
+    int8_t b;
+    __device__ __forceinline__ float get(int) const { return static_cast<float>(b); }
+};
+
+template <typename T, int U, int V>
+__global__ void __launch_bounds__(kRowThreads) rows_decode(const RowCodesParams P, uint32_t lanes) {
+    const Team team(lanes);
+    const uint32_t units = P.dim / U;
+    for (uint64_t r = team.first; r < P.rows; r += team.stride) {
+        const float s = P.scale_in ? __ldg(P.scale_in + r) : 1.0f;
+        const int8_t *codes = P.codes_in + r * P.dim;
         T *out = static_cast<T *>(P.out) + r * P.out_stride;
-        for (uint32_t j = threadIdx.x; j < P.dim; j += kRowThreads)
-            store_from_float(out + j, __fmul_rn(static_cast<float>(P.codes_in[r * P.dim + j]), s));
+        for (uint32_t base = team.lane; base < units; base += lanes * V) {
+            RawCodes<U> c[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (base + v * lanes < units)
+                    c[v] = *reinterpret_cast<const RawCodes<U> *>(codes + static_cast<uint64_t>(base + v * lanes) * U);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (base + v * lanes < units) {
+                    float f[U];
+#pragma unroll
+                    for (int j = 0; j < U; ++j) f[j] = __fmul_rn(c[v].get(j), s);
+                    store_values<T, U>(out + static_cast<uint64_t>(base + v * lanes) * U, f);
+                }
+        }
     }
 }
 
-__device__ __forceinline__ float sigmoid(float g) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-g))); }
-
-__device__ __forceinline__ float swiglu(float g, float u) {
-    return __fmul_rn(__fdiv_rn(g, __fadd_rn(1.0f, expf(-g))), u);
+// 1 / (1 + exp(-g)) by the hardware's exponential (base 2) and reciprocal: their
+// errors and the argument's rounding (|g| half units) stay below 2^-19 relative for
+// |g| < 16, an eighth of a per cent of half a code's step.  Saturates to 1 and 0.
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
+    return r;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) swiglu_encode(const SwigluParams P) {
-    __shared__ uint32_t red[kRowThreads / 32];
-    for (uint64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
+__device__ __forceinline__ float swiglu(float g, float u) { return __fmul_rn(__fmul_rn(g, sigmoid(g)), u); }
+
+template <typename T, int U, int V, int THREADS>
+__global__ void __launch_bounds__(THREADS) swiglu_encode(const SwigluParams P, uint32_t lanes) {
+    __shared__ uint32_t red[2][16][3];
+    using R = typename RawOf<T, U>::type;
+    const Team team(lanes);
+    const uint32_t units = P.dim / U, chunk = lanes * V;
+    int turn = 0;
+    for (uint64_t r0 = team.first - threadIdx.x / lanes; r0 < P.rows; r0 += team.stride) {
+        const uint64_t r = r0 + threadIdx.x / lanes;
+        const bool live = r < P.rows;
         const T *gate = static_cast<const T *>(P.in) + r * P.in_stride, *up = gate + P.dim;
-        uint32_t mg = 0, mu = 0, mh = 0;
-        for (uint32_t j = threadIdx.x; j < P.dim; j += kRowThreads) {
-            const float g = load_as_float(gate + j), u = load_as_float(up + j);
-            mg = max(mg, abs_bits(g));
-            mu = max(mu, abs_bits(u));
-            mh = max(mh, abs_bits(swiglu(g, u)));
+        R g[V], w[V];
+        float h[V][U];
+        uint32_t m[3] = {0, 0, 0};
+        auto load = [&](uint32_t base) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t u = base + v * lanes + team.lane;
+                if (live && u < units) {
+                    g[v] = load_unit<T, U>(gate + static_cast<uint64_t>(u) * U);
+                    w[v] = load_unit<T, U>(up + static_cast<uint64_t>(u) * U);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (live && base + v * lanes + team.lane < units)
+#pragma unroll
+                    for (int j = 0; j < U; ++j) h[v][j] = swiglu(g[v].get(j), w[v].get(j));
+        };
+        for (uint32_t base = 0; base < units; base += chunk) {
+            load(base);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (live && base + v * lanes + team.lane < units)
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        m[0] = max(m[0], abs_bits(g[v].get(j)));
+                        m[1] = max(m[1], abs_bits(w[v].get(j)));
+                        m[2] = max(m[2], abs_bits(h[v][j]));
+                    }
         }
-        const RowScale sg = row_scale_of(block_max(mg, red)), su = row_scale_of(block_max(mu, red)),
-                       sh = row_scale_of(block_max(mh, red));
-        int8_t *saved = P.saved_codes + r * 2 * P.dim;
-        for (uint32_t j = threadIdx.x; j < P.dim; j += kRowThreads) {
-            const float g = load_as_float(gate + j), u = load_as_float(up + j);
-            saved[j] = code_of(g, sg);
-            saved[P.dim + j] = code_of(u, su);
-            P.h_codes[r * P.dim + j] = code_of(swiglu(g, u), sh);
+        team_max(m, lanes, red, turn);
+        const RowScale sg = row_scale_of(m[0]), su = row_scale_of(m[1]), sh = row_scale_of(m[2]);
+        if (!live) continue;
+        int8_t *saved = P.saved_codes + r * 2 * P.dim, *out = P.h_codes + r * P.dim;
+        for (uint32_t base = 0; base < units; base += chunk) {
+            if (units > chunk) load(base);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t u = base + v * lanes + team.lane;
+                if (u < units) {
+                    const uint64_t at = static_cast<uint64_t>(u) * U;
+                    encode_unit<U>(saved + at, sg, [&](int j) { return g[v].get(j); });
+                    encode_unit<U>(saved + P.dim + at, su, [&](int j) { return w[v].get(j); });
+                    encode_unit<U>(out + at, sh, [&](int j) { return h[v][j]; });
+                }
+            }
         }
-        if (threadIdx.x == 0) {
+        if (team.lane == 0) {
             P.saved_scale[2 * r] = sg.scale;
             P.saved_scale[2 * r + 1] = su.scale;
             P.h_scale[r] = sh.scale;
@@ -88,47 +286,130 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_encode(const SwigluParams 
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowThreads) swiglu_backward(const SwigluParams P) {
-    for (uint64_t r = blockIdx.x; r < P.rows; r += gridDim.x) {
+template <typename T, int U, int V>
+__global__ void __launch_bounds__(kRowThreads) swiglu_backward(const SwigluParams P, uint32_t lanes) {
+    using R = typename RawOf<T, U>::type;
+    const Team team(lanes);
+    const uint32_t units = P.dim / U;
+    for (uint64_t r = team.first; r < P.rows; r += team.stride) {
         const T *dh = static_cast<const T *>(P.in) + r * P.in_stride;
         const int8_t *saved = P.saved_codes_in + r * 2 * P.dim;
-        const float sg = P.saved_scale_in[2 * r], su = P.saved_scale_in[2 * r + 1];
+        const float sg = __ldg(P.saved_scale_in + 2 * r), su = __ldg(P.saved_scale_in + 2 * r + 1);
         T *out = static_cast<T *>(P.dgate_up) + r * P.dgate_up_stride;
-        for (uint32_t j = threadIdx.x; j < P.dim; j += kRowThreads) {
-            const float g = __fmul_rn(static_cast<float>(saved[j]), sg);
-            const float u = __fmul_rn(static_cast<float>(saved[P.dim + j]), su);
-            const float d = load_as_float(dh + j), sig = sigmoid(g);
-            const float slope = __fmul_rn(sig, __fmaf_rn(g, __fsub_rn(1.0f, sig), 1.0f));
-            store_from_float(out + j, __fmul_rn(__fmul_rn(d, u), slope));
-            store_from_float(out + P.dim + j, __fmul_rn(d, __fmul_rn(g, sig)));
+        for (uint32_t base = team.lane; base < units; base += lanes * V) {
+            R d[V];
+            RawCodes<U> cg[V], cu[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (base + v * lanes < units) {
+                    const uint64_t at = static_cast<uint64_t>(base + v * lanes) * U;
+                    d[v] = load_unit<T, U>(dh + at);
+                    cg[v] = *reinterpret_cast<const RawCodes<U> *>(saved + at);
+                    cu[v] = *reinterpret_cast<const RawCodes<U> *>(saved + P.dim + at);
+                }
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (base + v * lanes < units) {
+                    const uint64_t at = static_cast<uint64_t>(base + v * lanes) * U;
+                    float dg[U], du[U];
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        const float g = __fmul_rn(cg[v].get(j), sg);
+                        const float u = __fmul_rn(cu[v].get(j), su);
+                        const float x = d[v].get(j), sig = sigmoid(g);
+                        const float slope = __fmul_rn(sig, __fmaf_rn(g, __fsub_rn(1.0f, sig), 1.0f));
+                        dg[j] = __fmul_rn(__fmul_rn(x, u), slope);
+                        du[j] = __fmul_rn(x, __fmul_rn(g, sig));
+                    }
+                    store_values<T, U>(out + at, dg);
+                    store_values<T, U>(out + P.dim + at, du);
+                }
         }
     }
 }
 
+// Lanes of a team that covers `units` with up to V units per lane: 8 to `most`.
+uint32_t lanes_for(uint32_t units, int v, uint32_t most) {
+    uint32_t lanes = 8;
+    while (lanes < most && lanes * v < units) lanes *= 2;
+    return lanes;
+}
+
 template <typename P>
-cudaError_t launch_rows(void (*kernel)(const P), const P &p, cudaStream_t stream) {
-    const int grid = persistent_grid(reinterpret_cast<const void *>(kernel), kRowThreads, p.rows);
-    kernel<<<grid, kRowThreads, 0, stream>>>(p);
+cudaError_t launch_rows(void (*kernel)(const P, uint32_t), const P &p, uint32_t lanes, int threads,
+                        cudaStream_t stream) {
+    const uint64_t teams = threads / lanes;
+    const int grid = persistent_grid(reinterpret_cast<const void *>(kernel), threads, (p.rows + teams - 1) / teams);
+    kernel<<<grid, threads, 0, stream>>>(p, lanes);
     return cudaGetLastError();
+}
+
+// Rows of the buffer start on a boundary of `bytes` and units of u elements fill them.
+bool fits(const void *p, uint64_t stride, size_t esize, uint32_t dim, uint32_t u, size_t bytes) {
+    return dim % u == 0 && reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * esize % bytes == 0;
+}
+
+template <typename T>
+cudaError_t encode_rows(const RowCodesParams &p, cudaStream_t stream) {
+    const uint32_t d = p.dim;
+    if (!fits(p.x, p.x_stride, sizeof(T), d, 8, 16) || !fits(p.codes, d, 1, d, 8, 8)) {
+        if (d <= 8 * kRowThreads) return launch_rows(rows_encode<T, 1, 8>, p, lanes_for(d, 8, kRowThreads), kRowThreads, stream);
+        return launch_rows(rows_encode<T, 1, 32>, p, kRowThreads, kRowThreads, stream);
+    }
+    const uint32_t units = d / 8;
+    if (units <= 32) return launch_rows(rows_encode<T, 8, 1>, p, lanes_for(units, 1, 32), kRowThreads, stream);
+    if (units <= 4 * kRowThreads) return launch_rows(rows_encode<T, 8, 4>, p, lanes_for(units, 4, kRowThreads), kRowThreads, stream);
+    return launch_rows(rows_encode<T, 8, 8>, p, kRowThreads, kRowThreads, stream);
+}
+
+template <typename T>
+cudaError_t decode_rows(const RowCodesParams &p, cudaStream_t stream) {
+    const uint32_t d = p.dim;
+    if (fits(p.out, p.out_stride, sizeof(T), d, 16, 16) && fits(p.codes_in, d, 1, d, 16, 16))
+        return launch_rows(rows_decode<T, 16, 4>, p, lanes_for(d / 16, 4, kRowThreads), kRowThreads, stream);
+    if (fits(p.out, p.out_stride, sizeof(T), d, 8, 16) && fits(p.codes_in, d, 1, d, 8, 8))
+        return launch_rows(rows_decode<T, 8, 4>, p, lanes_for(d / 8, 4, kRowThreads), kRowThreads, stream);
+    return launch_rows(rows_decode<T, 1, 8>, p, lanes_for(d, 8, kRowThreads), kRowThreads, stream);
+}
+
+template <typename T>
+cudaError_t encode_swiglu(const SwigluParams &p, cudaStream_t stream) {
+    const uint32_t d = p.dim;
+    // the ups start dim elements into a row: dim % 8 == 0 aligns them as the gates
+    if (!fits(p.in, p.in_stride, sizeof(T), d, 8, 16) || !fits(p.h_codes, d, 1, d, 8, 8) ||
+        !fits(p.saved_codes, 2 * d, 1, d, 8, 8))
+        return launch_rows(swiglu_encode<T, 1, 8, 512>, p, lanes_for(d, 8, 512), 512, stream);
+    const uint32_t units = d / 8;
+    if (units <= 64) return launch_rows(swiglu_encode<T, 8, 1, 256>, p, lanes_for(units, 1, 64), 256, stream);
+    if (units <= 1024) return launch_rows(swiglu_encode<T, 8, 2, 512>, p, lanes_for(units, 2, 512), 512, stream);
+    return launch_rows(swiglu_encode<T, 8, 4, 512>, p, 512, 512, stream);
+}
+
+template <typename T>
+cudaError_t backward_swiglu(const SwigluParams &p, cudaStream_t stream) {
+    const uint32_t d = p.dim;
+    if (fits(p.in, p.in_stride, sizeof(T), d, 8, 16) && fits(p.dgate_up, p.dgate_up_stride, sizeof(T), d, 8, 16) &&
+        fits(p.saved_codes_in, 2 * d, 1, d, 8, 8))
+        return launch_rows(swiglu_backward<T, 8, 2>, p, lanes_for(d / 8, 2, kRowThreads), kRowThreads, stream);
+    return launch_rows(swiglu_backward<T, 1, 4>, p, lanes_for(d, 4, kRowThreads), kRowThreads, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_rows_int8_encode(const RowCodesParams &p, int bf16, cudaStream_t stream) {
-    return launch_rows(bf16 ? rows_encode<uint16_t> : rows_encode<float>, p, stream);
+    return bf16 ? encode_rows<uint16_t>(p, stream) : encode_rows<float>(p, stream);
 }
 
 cudaError_t launch_rows_int8_decode(const RowCodesParams &p, int bf16, cudaStream_t stream) {
-    return launch_rows(bf16 ? rows_decode<uint16_t> : rows_decode<float>, p, stream);
+    return bf16 ? decode_rows<uint16_t>(p, stream) : decode_rows<float>(p, stream);
 }
 
 cudaError_t launch_swiglu_encode(const SwigluParams &p, int bf16, cudaStream_t stream) {
-    return launch_rows(bf16 ? swiglu_encode<uint16_t> : swiglu_encode<float>, p, stream);
+    return bf16 ? encode_swiglu<uint16_t>(p, stream) : encode_swiglu<float>(p, stream);
 }
 
 cudaError_t launch_swiglu_backward(const SwigluParams &p, int bf16, cudaStream_t stream) {
-    return launch_rows(bf16 ? swiglu_backward<uint16_t> : swiglu_backward<float>, p, stream);
+    return bf16 ? backward_swiglu<uint16_t>(p, stream) : backward_swiglu<float>(p, stream);
 }
 
 }  // namespace qc

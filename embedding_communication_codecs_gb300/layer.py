@@ -209,6 +209,14 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
+def _raw_stream(stream, t):
+    """The stream's handle; without one, the current stream of t's device (one lookup,
+    without the Stream object that torch.cuda.current_stream() builds)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
+
+
 def _scratch(nbytes, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
@@ -224,7 +232,7 @@ def rowwise_int8(x, *, stream=None):
         codes = torch.empty((rows, dim), dtype=torch.int8, device=x.device)
         scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
         _check(lib.qc_rowwise_int8(x.data_ptr(), _CODE_OF[x.dtype], stride, rows, dim, codes.data_ptr(),
-                                   scale.data_ptr(), _stream(stream)))
+                                   scale.data_ptr(), _raw_stream(stream, x)))
     return codes, scale
 
 
@@ -236,7 +244,7 @@ def rowwise_int8_dequant(codes, row_scale, *, dtype=torch.bfloat16, stream=None)
     with _on(stream):
         out = torch.empty((rows, dim), dtype=dtype, device=codes.device)
         _check(lib.qc_rowwise_int8_dequant(codes.data_ptr(), row_scale.data_ptr(), rows, dim,
-                                           out.data_ptr(), code, dim, _stream(stream)))
+                                           out.data_ptr(), code, dim, _raw_stream(stream, codes)))
     return out
 
 
@@ -257,7 +265,7 @@ def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bf
         ws = _scratch(nbytes, x_codes.device)
         _check(lib.qc_int8_matmul(x_codes.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
                                   w_scale.data_ptr(), _ptr(bias), T, N, K, y.data_ptr(), code, N,
-                                  _ptr(ws), nbytes, _stream(stream)))
+                                  _ptr(ws), nbytes, _raw_stream(stream, x_codes)))
     return y
 
 
@@ -275,7 +283,7 @@ def int8_input_grad(dy, w_codes, w_scale, *, dtype=torch.bfloat16, stream=None):
         nbytes = lib.qc_int8_input_grad_workspace(T, N, K)
         ws = _scratch(nbytes, dy.device)
         _check(lib.qc_int8_input_grad(dy.data_ptr(), stride, w_codes.data_ptr(), w_scale.data_ptr(), T, N,
-                                      K, dx.data_ptr(), code, K, _ptr(ws), nbytes, _stream(stream)))
+                                      K, dx.data_ptr(), code, K, _ptr(ws), nbytes, _raw_stream(stream, dy)))
     return dx
 
 
@@ -307,7 +315,7 @@ def int8_weight_grad(dy, x_codes, x_scale, *, dtype=torch.float32, with_bias=Fal
         _check(lib.qc_int8_weight_grad(dy.data_ptr(), stride, x_codes.data_ptr(), x_scale.data_ptr(), T, N,
                                        K, dw.data_ptr(), code, _ptr(dbias),
                                        0 if into is None else QC_ACCUMULATE_INTO_OUT, _ptr(ws), nbytes,
-                                       _stream(stream)))
+                                       _raw_stream(stream, dy)))
     return dw, dbias
 
 
@@ -327,7 +335,7 @@ def swiglu_encode(gate_up, *, stream=None):
         saved_scale = torch.empty((rows, 2), dtype=torch.float32, device=dev)
         _check(lib.qc_swiglu_encode(gate_up.data_ptr(), _CODE_OF[gate_up.dtype], stride, rows, dim,
                                     h_codes.data_ptr(), h_scale.data_ptr(), saved_codes.data_ptr(),
-                                    saved_scale.data_ptr(), _stream(stream)))
+                                    saved_scale.data_ptr(), _raw_stream(stream, gate_up)))
     return h_codes, h_scale, saved_codes, saved_scale
 
 
@@ -343,5 +351,5 @@ def swiglu_backward(dh, saved_codes, saved_scale, *, stream=None):
         out = torch.empty((rows, 2 * dim), dtype=dh.dtype, device=dh.device)
         _check(lib.qc_swiglu_backward(dh.data_ptr(), _CODE_OF[dh.dtype], stride, saved_codes.data_ptr(),
                                       saved_scale.data_ptr(), rows, dim, out.data_ptr(), 2 * dim,
-                                      _stream(stream)))
+                                      _raw_stream(stream, dh)))
     return out
