@@ -14,12 +14,12 @@
 //
 // A pair of blocks (a cluster of two) owns a 256 x BN tile: each holds 128 rows of A
 // and BN / 2 rows of B per step of 64 along l, and 128 x BN sums in its tensor
-// memory, twice, so that one tile is stored while the next is summed.  Warp 0 loads
-// (TMA), warp 1 of the leading block issues the matrix instructions, warps 2 to 5
-// store.  Every wait is bounded (qc_pipeline.cuh).
+// memory, twice, so that one is read while the next is summed.  Warp 0 loads (TMA),
+// warp 1 of the leading block issues the matrix instructions, warps 2 to 9 add the
+// parts of a sum and store.  Every wait is bounded (qc_pipeline.cuh).
 #include <cuda.h>
 
-#include <mutex>
+#include <atomic>
 
 #include "qc_int8_rows.cuh"
 #include "qc_internal.h"
@@ -35,8 +35,14 @@ namespace {
 constexpr int kStep = 64;       // contraction elements per stage: one 128-byte row
 constexpr int kBlockM = 128;    // rows of A per block
 constexpr int kPairM = 2 * kBlockM;
-constexpr int kGemmThreads = 192;
+constexpr int kStoreWarps = 8;
+constexpr int kGemmThreads = 32 * (2 + kStoreWarps);
 constexpr int kGroupM = 8;      // tiles along M that share their B tiles in L2
+// The tensor core's running sum loses up to a unit in the last place per
+// instruction, always towards zero, so its error grows with the length of the sum
+// (1.1e-6 of the result after 8192 terms, measured).  A sum is cut into parts of
+// 32 steps = 2048 terms, which the storing warps add in fp32, rounding to nearest.
+constexpr uint32_t kPartSteps = 32;
 
 template <int BN>
 struct Tile {
@@ -45,11 +51,15 @@ struct Tile {
     static constexpr int kStage = kBytesA + kBytesB;
     static constexpr int kStages = BN == 256 ? 6 : 8;
     static constexpr int kTmemCols = 2 * BN;
-    static constexpr int kSmem = kStages * kStage + 1024;  // tiles start on 1024 bytes
+    static constexpr int kWarpCols = BN / 2;               // columns of a storing warp
+    static constexpr int kTurn = kStoreWarps * 32 * 33 * 4;        // store_anywhere()
+    static constexpr int kSmem = kStages * kStage + kTurn + 1024;  // tiles start on 1024 bytes
 };
 
 struct GemmParams {
     uint64_t M, N, L;
+    uint32_t splits, split_steps;  // the contraction in `splits` ranges of split_steps steps
+    float *partial;                // splits x M x N sums, where splits > 1
     void *out;
     uint64_t out_stride;
     int out_bf16, accumulate, vector_out;
@@ -57,14 +67,20 @@ struct GemmParams {
     uint32_t *status;
 };
 
-// Tile t of the grid of 256 x BN tiles: groups of kGroupM tile rows, column by column
-// inside a group.
-__device__ __forceinline__ void tile_at(uint32_t t, uint32_t tiles_m, uint32_t tiles_n, uint32_t &m, uint32_t &n) {
+// A pair's unit of work: one tile, one range of the contraction.
+struct Unit {
+    uint32_t m, n, split, first_step, steps;
+};
+
+// Units in order: all tiles of the first range, then of the next.  Tiles in groups
+// of kGroupM tile rows, column by column inside a group.
+__device__ __forceinline__ Unit unit_at(uint32_t u, uint32_t tiles_m, uint32_t tiles_n, const GemmParams &P) {
+    const uint32_t ntiles = tiles_m * tiles_n, split = u / ntiles, t = u % ntiles;
     const uint32_t per_group = kGroupM * tiles_n;
     const uint32_t g = t / per_group, r = t % per_group;
     const uint32_t rows = min(tiles_m - g * kGroupM, static_cast<uint32_t>(kGroupM));
-    m = g * kGroupM + r % rows;
-    n = r / rows;
+    const uint32_t all = static_cast<uint32_t>((P.L + kStep - 1) / kStep), first = split * P.split_steps;
+    return {g * kGroupM + r % rows, r / rows, split, first, min(P.split_steps, all - first)};
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -73,52 +89,77 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-// 32 sums of row m from column n on: scale, bias, store.
-__device__ __forceinline__ void store_chunk(const GemmParams &P, uint64_t m, uint64_t n, const uint32_t (&acc)[32]) {
-    float v[32];
+// One result from its whole sum.
+__device__ __forceinline__ float finish(const GemmParams &P, uint64_t m, uint64_t n, float v) {
+    if (P.m_scale) v = __fmul_rn(v, __fmul_rn(__ldg(P.m_scale + m), __ldg(P.n_scale + n)));
+    return P.bias ? __fadd_rn(v, __ldg(P.bias + n)) : v;
+}
+
+// A storing warp's C columns of row m (its lane's) from column n on, a vector at a
+// time: whole columns, rows on 16-byte boundaries.
+template <int C>
+__device__ __forceinline__ void store_vectors(const GemmParams &P, uint32_t split, uint64_t m, uint64_t n,
+                                              const float (&acc)[C]) {
+    if (P.splits > 1) {
+        float *o = P.partial + (split * P.M + m) * P.N + n;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(acc[j]);
-    const bool whole = n + 32 <= P.N;
-    if (P.m_scale) {
-        const float ms = __ldg(P.m_scale + m);
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (whole || n + j < P.N) v[j] = __fmul_rn(v[j], __fmul_rn(ms, __ldg(P.n_scale + n + j)));
-    }
-    if (P.bias) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (whole || n + j < P.N) v[j] = __fadd_rn(v[j], __ldg(P.bias + n + j));
-    }
-    if (P.out_bf16) {
+        for (int c = 0; c < C; c += 4)
+            *reinterpret_cast<float4 *>(o + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
+    } else if (P.out_bf16) {
         uint16_t *o = static_cast<uint16_t *>(P.out) + m * P.out_stride + n;
-        if (whole && P.vector_out) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8)
-                *reinterpret_cast<uint4 *>(o + j) = make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]),
-                                                               pack_bf16(v[j + 4], v[j + 5]), pack_bf16(v[j + 6], v[j + 7]));
-        } else {
+        for (int c = 0; c < C; c += 8) {
+            float v[8];
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (n + j < P.N) o[j] = to_bf16(v[j]);
+            for (int j = 0; j < 8; ++j) v[j] = finish(P, m, n + c + j, acc[c + j]);
+            *reinterpret_cast<uint4 *>(o + c) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                           pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
         }
     } else {
         float *o = static_cast<float *>(P.out) + m * P.out_stride + n;
-        if (whole && P.vector_out) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                if (P.accumulate) {
-                    const float4 c = *reinterpret_cast<const float4 *>(o + j);
-                    w = make_float4(__fadd_rn(c.x, w.x), __fadd_rn(c.y, w.y), __fadd_rn(c.z, w.z), __fadd_rn(c.w, w.w));
-                }
-                *reinterpret_cast<float4 *>(o + j) = w;
+        for (int c = 0; c < C; c += 4) {
+            float4 v = make_float4(finish(P, m, n + c, acc[c]), finish(P, m, n + c + 1, acc[c + 1]),
+                                   finish(P, m, n + c + 2, acc[c + 2]), finish(P, m, n + c + 3, acc[c + 3]));
+            if (P.accumulate) {
+                const float4 w = *reinterpret_cast<const float4 *>(o + c);
+                v = make_float4(__fadd_rn(w.x, v.x), __fadd_rn(w.y, v.y), __fadd_rn(w.z, v.z), __fadd_rn(w.w, v.w));
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (n + j < P.N) o[j] = P.accumulate ? __fadd_rn(o[j], v[j]) : v[j];
+            *reinterpret_cast<float4 *>(o + c) = v;
         }
+    }
+}
+
+// The same at an edge of the matrix or where rows start anywhere: 32 x 32 sums are
+// turned in the warp's shared memory, so that its lanes store neighbouring columns
+// of one row.  m0 is the warp's first row.
+template <int C>
+__device__ __forceinline__ void store_anywhere(const GemmParams &P, uint32_t split, uint64_t m0, uint64_t n, int lane,
+                                               float (*turn)[33], const float (&acc)[C]) {
+    const int rows = P.M - m0 < 32 ? static_cast<int>(P.M - m0) : 32;
+#pragma unroll
+    for (int c = 0; c < C; c += 32) {
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) turn[lane][j] = acc[c + j];
+        __syncwarp();
+        const uint64_t col = n + c + lane;
+        if (col < P.N)
+            for (int r = 0; r < rows; ++r) {
+                const float sum = turn[r][lane];
+                const uint64_t m = m0 + r;
+                if (P.splits > 1) {
+                    P.partial[(split * P.M + m) * P.N + col] = sum;
+                    continue;
+                }
+                const float v = finish(P, m, col, sum);
+                if (P.out_bf16) {
+                    static_cast<uint16_t *>(P.out)[m * P.out_stride + col] = to_bf16(v);
+                } else {
+                    float *o = static_cast<float *>(P.out) + m * P.out_stride + col;
+                    *o = P.accumulate ? __fadd_rn(*o, v) : v;
+                }
+            }
     }
 }
 
@@ -131,12 +172,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     __shared__ uint64_t full[S], empty[S], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_slot;
     uint8_t *const tiles = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    float(*const turn)[32][33] = reinterpret_cast<float(*)[32][33]>(tiles + S * T::kStage);  // one per storing warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t tiles_m = static_cast<uint32_t>((P.M + kPairM - 1) / kPairM);
     const uint32_t tiles_n = static_cast<uint32_t>((P.N + BN - 1) / BN);
-    const uint32_t ntiles = tiles_m * tiles_n, npairs = gridDim.x / 2, pair = blockIdx.x / 2;
-    const uint32_t steps = static_cast<uint32_t>((P.L + kStep - 1) / kStep);
+    const uint32_t units = tiles_m * tiles_n * P.splits, npairs = gridDim.x / 2, pair = blockIdx.x / 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -145,7 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&sums_full[b], 1);
-            mbar_init(&sums_empty[b], 8);  // four storing warps in each block
+            mbar_init(&sums_empty[b], 2 * kStoreWarps);  // the storing warps of both blocks
         }
         mbar_init(&drained, 1);
         fence_barrier_init();
@@ -165,12 +206,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
-            for (uint32_t t = pair; t < ntiles && ok; t += npairs) {
-                uint32_t tm, tn;
-                tile_at(t, tiles_m, tiles_n, tm, tn);
-                const int m0 = static_cast<int>(tm * kPairM + rank * kBlockM);
-                const int n0 = static_cast<int>(tn * BN + rank * T::kRowsB);
-                for (uint32_t k = 0; k < steps; ++k, ++it) {
+            for (uint32_t u = pair; u < units && ok; u += npairs) {
+                const Unit w = unit_at(u, tiles_m, tiles_n, P);
+                const int m0 = static_cast<int>(w.m * kPairM + rank * kBlockM);
+                const int n0 = static_cast<int>(w.n * BN + rank * T::kRowsB);
+                for (uint32_t k = 0; k < w.steps; ++k, ++it) {
                     const uint32_t s = it % S, phase = (it / S) & 1;
                     if (!mbar_wait_cluster(&empty[s], phase ^ 1)) {
                         ok = false;
@@ -179,7 +219,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                     const uint32_t bar = in_block(&full[s], 0);
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * T::kStage);
                     uint8_t *a = tiles + s * T::kStage, *b = a + T::kBytesA;
-                    const int l0 = static_cast<int>(k * kStep);
+                    const int l0 = static_cast<int>((w.first_step + k) * kStep);
                     if (A_MN) {
                         tma_load_pair(a, &map_a, m0, l0, bar);
                         tma_load_pair(a + T::kBytesA / 2, &map_a, m0 + 64, l0, bar);
@@ -204,29 +244,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             constexpr uint32_t kInstr = bf16_instruction(kPairM, BN, A_MN, B_MN);
             // 16 contraction elements on: 32 bytes inside a row, or 16 rows of 128 bytes
             constexpr uint32_t kNextA = (A_MN ? 2048 : 32) >> 4, kNextB = (B_MN ? 2048 : 32) >> 4;
-            uint32_t it = 0, i = 0;
-            for (uint32_t t = pair; t < ntiles && ok; t += npairs, ++i) {
-                const uint32_t buf = i & 1;
-                if (!mbar_wait_cluster(&sums_empty[buf], ((i >> 1) & 1) ^ 1)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                for (uint32_t k = 0; k < steps; ++k, ++it) {
-                    const uint32_t s = it % S;
-                    if (!mbar_wait_cluster(&full[s], (it / S) & 1)) {
+            uint32_t it = 0, part = 0;  // parts so far: the two sums in tensor memory are used in turn
+            for (uint32_t u = pair; u < units && ok; u += npairs) {
+                const uint32_t steps = unit_at(u, tiles_m, tiles_n, P).steps;
+                for (uint32_t k0 = 0; k0 < steps && ok; k0 += kPartSteps, ++part) {
+                    const uint32_t buf = part & 1, k1 = min(k0 + kPartSteps, steps);
+                    if (!mbar_wait_cluster(&sums_empty[buf], ((part >> 1) & 1) ^ 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t a = smem_operand(tiles + s * T::kStage, 64 * kStep * 2);
-                    const uint64_t b = smem_operand(tiles + s * T::kStage + T::kBytesA, 64 * kStep * 2);
+                    for (uint32_t k = k0; k < k1; ++k, ++it) {
+                        const uint32_t s = it % S;
+                        if (!mbar_wait_cluster(&full[s], (it / S) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t a = smem_operand(tiles + s * T::kStage, 64 * kStep * 2);
+                        const uint64_t b = smem_operand(tiles + s * T::kStage + T::kBytesA, 64 * kStep * 2);
 #pragma unroll
-                    for (int j = 0; j < kStep / 16; ++j)
-                        mma_pair(tmem + buf * BN, a + j * kNextA, b + j * kNextB, kInstr, (k | j) != 0);
-                    mma_commit_pair(&empty[s]);
+                        for (int j = 0; j < kStep / 16; ++j)
+                            mma_pair(tmem + buf * BN, a + j * kNextA, b + j * kNextB, kInstr, k > k0 || j > 0);
+                        mma_commit_pair(&empty[s]);
+                    }
+                    mma_commit_pair(&sums_full[buf]);
                 }
-                mma_commit_pair(&sums_full[buf]);
             }
             mma_commit_pair(&drained);
         }
@@ -234,31 +277,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         // arrivals that it sent to both blocks
         if (lane == 0) ok &= mbar_wait_cluster(&drained, 0);
     } else {
-        const int quarter = warp & 3;  // the 32 lanes of tensor memory that this warp may read
-        uint32_t i = 0;
-        for (uint32_t t = pair; t < ntiles; t += npairs, ++i) {
-            uint32_t tm, tn;
-            tile_at(t, tiles_m, tiles_n, tm, tn);
-            const uint32_t buf = i & 1;
-            ok = mbar_wait_cluster(&sums_full[buf], (i >> 1) & 1);
-            if (__any_sync(kFull, !ok)) {
-                ok = false;
-                break;
+        const int quarter = warp & 3;                         // the 32 lanes of tensor memory that this warp may read
+        const uint32_t c0 = (warp - 2) / 4 * T::kWarpCols;    // its half of the columns
+        const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+        uint32_t part = 0;
+        for (uint32_t u = pair; u < units && ok; u += npairs) {
+            const Unit w = unit_at(u, tiles_m, tiles_n, P);
+            float acc[T::kWarpCols];
+            for (uint32_t k0 = 0; k0 < w.steps; k0 += kPartSteps, ++part) {
+                const uint32_t buf = part & 1;
+                ok = mbar_wait_cluster(&sums_full[buf], (part >> 1) & 1);
+                if (__any_sync(kFull, !ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < T::kWarpCols; c += 16) {
+                    uint32_t v[16];
+                    tmem_load16(from + buf * BN + c, v);
+                    tmem_wait_load();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        acc[c + j] = k0 == 0 ? __uint_as_float(v[j]) : __fadd_rn(acc[c + j], __uint_as_float(v[j]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(in_block(&sums_empty[buf], 0));
             }
-            tc_fence_after();
-            const uint64_t m = static_cast<uint64_t>(tm) * kPairM + rank * kBlockM + quarter * 32 + lane;
-#pragma unroll 1
-            for (int c = 0; c < BN; c += 32) {
-                const uint64_t n = static_cast<uint64_t>(tn) * BN + c;
-                if (n >= P.N) break;
-                uint32_t acc[32];
-                tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BN + c, acc);
-                tmem_wait_load();
-                if (m < P.M) store_chunk(P, m, n, acc);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(in_block(&sums_empty[buf], 0));
+            if (!ok) break;
+            const uint64_t m0 = static_cast<uint64_t>(w.m) * kPairM + rank * kBlockM + quarter * 32;
+            const uint64_t n = static_cast<uint64_t>(w.n) * BN + c0;
+            if (m0 >= P.M || n >= P.N) continue;
+            if (P.vector_out && m0 + 32 <= P.M && n + T::kWarpCols <= P.N)
+                store_vectors<T::kWarpCols>(P, w.split, m0 + lane, n, acc);
+            else
+                store_anywhere<T::kWarpCols>(P, w.split, m0, n, lane, turn[warp - 2], acc);
         }
     }
     if (!ok) report_failure(&g_product_error, P.status, kErrPipelineTimeout);
@@ -266,6 +320,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     cluster_sync();
     if (warp == 1) tmem_free_pair<T::kTmemCols>(tmem);
+}
+
+// The ranges of a split contraction, added in order: Q columns of a row per thread.
+template <int Q>
+__global__ void __launch_bounds__(256) join(const GemmParams P) {
+    const uint64_t per_row = P.N / Q, total = P.M * per_row;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<uint64_t>(gridDim.x) * 256) {
+        const uint64_t m = i / per_row, n = i % per_row * Q;
+        float v[Q] = {};
+        for (uint32_t s = 0; s < P.splits; ++s) {
+            const float *p = P.partial + (s * P.M + m) * P.N + n;
+            if constexpr (Q == 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(p);
+                v[0] = __fadd_rn(v[0], w.x);
+                v[1] = __fadd_rn(v[1], w.y);
+                v[2] = __fadd_rn(v[2], w.z);
+                v[3] = __fadd_rn(v[3], w.w);
+            } else {
+                v[0] = __fadd_rn(v[0], *p);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < Q; ++j) {
+            const float r = finish(P, m, n + j, v[j]);
+            if (P.out_bf16) {
+                static_cast<uint16_t *>(P.out)[m * P.out_stride + n + j] = to_bf16(r);
+            } else {
+                float *o = static_cast<float *>(P.out) + m * P.out_stride + n + j;
+                *o = P.accumulate ? __fadd_rn(*o, r) : r;
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------------------ the host
@@ -307,8 +393,57 @@ bool tma_fits(const void *p, uint64_t stride) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
 }
 
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
+    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) return 1;
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// How a product of M x N results over L terms is cut.
+struct Plan {
+    int bn;
+    uint32_t splits, split_steps;
+};
+
+constexpr uint32_t kMaxSplits = 16;
+
+// The cheapest of a few cuts by an estimate in SM cycles: a pair goes through
+// ceil(units / pairs) units, each of its steps at 512 or 256 cycles (the tensor
+// core's rate for 256 x BN x 64) plus a start and a store of about 3000; a split one
+// also writes and reads its sums (about 2500 bytes a cycle) in a second launch.
+// `pairs` is fixed, so that the workspace's size does not depend on the device.
+Plan plan_for(uint64_t M, uint64_t N, uint64_t L) {
+    constexpr uint64_t kPairs = 76;
+    const uint64_t steps = (L + kStep - 1) / kStep;
+    Plan best{256, 1, static_cast<uint32_t>(steps)};
+    double best_cost = 1e300;
+    for (int bn : {256, 128}) {
+        const uint64_t tiles = ((M + kPairM - 1) / kPairM) * ((N + bn - 1) / bn);
+        for (uint32_t s = 1; s <= kMaxSplits && (s == 1 || (steps / s >= 4 && tiles < kPairs)); ++s) {
+            const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
+            const uint64_t waves = (tiles * splits + kPairs - 1) / kPairs;
+            double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bn == 256 ? 512 : 280) + 3000);
+            if (splits > 1) cost += 6000 + static_cast<double>(splits) * M * N * 8 / 2500;
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = {bn, static_cast<uint32_t>(splits), static_cast<uint32_t>(per)};
+            }
+        }
+    }
+    return best;
+}
+
+uint64_t partial_bytes(uint64_t M, uint64_t N, uint64_t L) {
+    const Plan p = plan_for(M, N, L);
+    return p.splits > 1 ? (p.splits * M * N * 4 + 255) / 256 * 256 : 0;
+}
+
 template <int BN, bool A_MN, bool B_MN>
-cudaError_t launch_gemm(const Operand &a, const Operand &b, GemmParams g, cudaStream_t stream) {
+cudaError_t launch_gemm(const Operand &a, const Operand &b, const GemmParams &g, cudaStream_t stream) {
     using T = Tile<BN>;
     const auto kernel = gemm<BN, A_MN, B_MN>;
     CUtensorMap ma, mb;
@@ -317,22 +452,30 @@ cudaError_t launch_gemm(const Operand &a, const Operand &b, GemmParams g, cudaSt
         return cudaErrorInvalidValue;
     cudaError_t e = prepare_dynamic_smem(reinterpret_cast<const void *>(kernel), T::kSmem);
     if (e != cudaSuccess) return e;
-    const uint64_t ntiles = ((g.M + kPairM - 1) / kPairM) * ((g.N + BN - 1) / BN);
-    if (ntiles > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
-    const int esize = g.out_bf16 ? 2 : 4;
-    g.vector_out = (reinterpret_cast<uintptr_t>(g.out) & 15) == 0 && (g.out_stride * esize) % 16 == 0;
-    // one block per SM, in pairs
-    int dev = 0, sms = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const uint64_t pairs = ntiles < static_cast<uint64_t>(sms / 2) ? ntiles : sms / 2;
-    kernel<<<static_cast<unsigned>(2 * pairs), kGemmThreads, T::kSmem, stream>>>(ma, mb, g);
+    const uint64_t units = ((g.M + kPairM - 1) / kPairM) * ((g.N + BN - 1) / BN) * g.splits;
+    if (units > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
+    const uint64_t most = sm_count() / 2;  // one block per SM, in pairs
+    kernel<<<static_cast<unsigned>(2 * (units < most ? units : most)), kGemmThreads, T::kSmem, stream>>>(ma, mb, g);
     return cudaGetLastError();
 }
 
 template <bool A_MN, bool B_MN>
-cudaError_t launch_product(const Operand &a, const Operand &b, const GemmParams &g, cudaStream_t stream) {
-    return launch_gemm<256, A_MN, B_MN>(a, b, g, stream);
+cudaError_t launch_product(const Operand &a, const Operand &b, GemmParams g, void *partial, cudaStream_t stream) {
+    const Plan plan = plan_for(g.M, g.N, g.L);
+    g.splits = plan.splits;
+    g.split_steps = plan.split_steps;
+    g.partial = static_cast<float *>(partial);
+    const int esize = g.out_bf16 ? 2 : 4;
+    g.vector_out = g.splits > 1 ? g.N % 4 == 0
+                                : (reinterpret_cast<uintptr_t>(g.out) & 15) == 0 && (g.out_stride * esize) % 16 == 0;
+    const cudaError_t e = plan.bn == 256 ? launch_gemm<256, A_MN, B_MN>(a, b, g, stream)
+                                         : launch_gemm<128, A_MN, B_MN>(a, b, g, stream);
+    if (e != cudaSuccess || g.splits == 1) return e;
+    const auto kernel = g.N % 4 == 0 ? join<4> : join<1>;
+    const uint64_t work = g.M * (g.N % 4 == 0 ? g.N / 4 : g.N);
+    const int grid = persistent_grid(reinterpret_cast<const void *>(kernel), 256, (work + 255) / 256);
+    kernel<<<grid, 256, 0, stream>>>(g);
+    return cudaGetLastError();
 }
 
 __global__ void column_sums(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t cols, float *out,
@@ -396,13 +539,13 @@ GemmParams outputs(const ProductParams &p, uint64_t M, uint64_t N, uint64_t L) {
 }  // namespace
 
 size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K) {
-    return widened_bytes(T, K) + widened_bytes(N, K);
+    return widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K);
 }
 size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
-    return widened_bytes(N, K) + widened_bytes(T, N);
+    return widened_bytes(N, K) + widened_bytes(T, N) + partial_bytes(T, K, N);
 }
 size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
-    return widened_bytes(T, K) + widened_bytes(T, N);
+    return widened_bytes(T, K) + widened_bytes(T, N) + partial_bytes(N, K, T);
 }
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
@@ -415,7 +558,7 @@ cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
     g.m_scale = p.x_scale;
     g.n_scale = p.w_scale;
     g.bias = p.bias;
-    return launch_product<false, false>(x, w, g, stream);
+    return launch_product<false, false>(x, w, g, ws + widened_bytes(p.T, p.K) + widened_bytes(p.N, p.K), stream);
 }
 
 cudaError_t launch_int8_input_grad(const ProductParams &p, cudaStream_t stream) {
@@ -424,7 +567,8 @@ cudaError_t launch_int8_input_grad(const ProductParams &p, cudaStream_t stream) 
     cudaError_t e = widen(p.w_codes, p.w_scale, p.N, p.K, ws, w, stream);
     if (e == cudaSuccess) e = readable_dy(p, ws + widened_bytes(p.N, p.K), dy, stream);
     if (e != cudaSuccess) return e;
-    return launch_product<false, true>(dy, w, outputs(p, p.T, p.K, p.N), stream);
+    return launch_product<false, true>(dy, w, outputs(p, p.T, p.K, p.N),
+                                       ws + widened_bytes(p.N, p.K) + widened_bytes(p.T, p.N), stream);
 }
 
 cudaError_t launch_int8_weight_grad(const ProductParams &p, cudaStream_t stream) {
@@ -438,7 +582,8 @@ cudaError_t launch_int8_weight_grad(const ProductParams &p, cudaStream_t stream)
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     e = widen(p.x_codes, p.x_scale, p.T, p.K, ws, x, stream);
     if (e == cudaSuccess) e = readable_dy(p, ws + widened_bytes(p.T, p.K), dy, stream);
-    if (e == cudaSuccess) e = launch_product<true, true>(dy, x, outputs(p, p.N, p.K, p.T), stream);
+    if (e == cudaSuccess) e = launch_product<true, true>(dy, x, outputs(p, p.N, p.K, p.T),
+                                       ws + widened_bytes(p.T, p.K) + widened_bytes(p.T, p.N), stream);
     if (e != cudaSuccess || !p.dbias) return e;
     column_sums<<<static_cast<unsigned>((p.N + 127) / 128), 128, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N,
                                                                               p.dbias, p.accumulate);
