@@ -1,0 +1,184 @@
+// qc_int8_few.cu -- the product of the 8-bit layer for few tokens (one new token per
+// request).
+//
+// The weights' N K bytes are read once and bound it.  A block owns 16 MT outputs for
+// 8 NT tokens; its eight warps take 64-element chunks of the contraction in turn.
+// A lane loads 16 consecutive codes of a weight row (eight rows of 64 bytes per
+// instruction) and the same 16 of a token, and widens both to f16 in registers
+// (exactly: |code| <= 128) as fragments of m16n8k16 matrix instructions.  The order
+// of the contraction inside a fragment is free, as long as both operands use the
+// same one, so the codes need no shuffle: bytes 4j .. 4j+3 of a lane are its share
+// of the j-th instruction.  The warps' sums meet in shared memory and are added in
+// order.  (mma.sync runs at 300 T multiply-adds/s here for f16 and 75 for int8,
+// measured: at 16 tokens the weights' stream already needs 107.)
+#include "qc_int8_rows.cuh"
+#include "qc_internal.h"
+
+namespace qc {
+namespace {
+
+constexpr int kFewWarps = 8;
+constexpr int kChunk = 64;
+
+struct FewParams {
+    const int8_t *x, *w;
+    const float *x_scale, *w_scale, *bias;
+    uint64_t T, N, K;
+    void *y;
+    uint64_t y_stride;
+    int y_bf16;
+};
+
+// Four codes -> two f16 pairs: each byte, offset by 128, under the exponent of
+// 2^10 (1024 + 128 + code), minus 1152.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    w ^= 0x80808080u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The aligned word at `p`, of which only the bytes inside [begin, end) are read.
+__device__ __forceinline__ uint32_t word_inside(const uint8_t *p, const uint8_t *begin, const uint8_t *end) {
+    if (p >= begin && p + 4 <= end) return __ldg(reinterpret_cast<const uint32_t *>(p));
+    uint32_t v = 0;
+    for (int i = 0; i < 4; ++i)
+        if (p + i >= begin && p + i < end) v |= static_cast<uint32_t>(__ldg(p + i)) << (8 * i);
+    return v;
+}
+
+// 16 codes from element k of a row on, zeros from K on.  ALIGNED: every row starts
+// on 16 bytes and K is a multiple of 16; otherwise the words around them are read
+// and shifted.
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 load16(const int8_t *base, uint64_t row, uint64_t k, uint64_t rows, uint64_t K) {
+    if (row >= rows || k >= K) return make_uint4(0u, 0u, 0u, 0u);
+    const int8_t *p = base + row * K + k;
+    if constexpr (ALIGNED) {
+        return __ldg(reinterpret_cast<const uint4 *>(p));
+    } else {
+        const uint8_t *begin = reinterpret_cast<const uint8_t *>(base), *end = begin + rows * K;
+        const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+        const uint8_t *q = reinterpret_cast<const uint8_t *>(p) - off;
+        uint32_t v[5], r[4];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) v[i] = word_inside(q + 4 * i, begin, end);
+        const uint64_t left = K - k;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r[i] = __funnelshift_r(v[i], v[i + 1], 8 * off);
+            if (left < 4u * i + 4u) r[i] = left <= 4u * i ? 0u : r[i] & (0xFFFFFFFFu >> (32 - 8 * (left - 4 * i)));
+        }
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    }
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int j) {
+    return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
+
+// AHEAD chunks of a warp are loaded before the first of them is multiplied.
+template <int NT, int MT, int AHEAD, bool ALIGNED>
+__global__ void __launch_bounds__(32 * kFewWarps) few_tokens(const FewParams P) {
+    extern __shared__ float sums[];  // [warp][token][output], outputs padded by one
+    constexpr int kOut = 16 * MT, kTok = 8 * NT, kPitch = kOut + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const uint64_t n0 = static_cast<uint64_t>(blockIdx.x) * kOut, t0 = static_cast<uint64_t>(blockIdx.y) * kTok;
+    float acc[MT][NT][4] = {};
+    const uint64_t step = kFewWarps * kChunk;
+    for (uint64_t k0 = static_cast<uint64_t>(warp) * kChunk; k0 < P.K; k0 += AHEAD * step) {
+        uint4 w[AHEAD][MT][2], x[AHEAD][NT];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const uint64_t k = k0 + a * step + 16 * q;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                w[a][i][0] = load16<ALIGNED>(P.w, n0 + 16 * i + g, k, P.N, P.K);
+                w[a][i][1] = load16<ALIGNED>(P.w, n0 + 16 * i + g + 8, k, P.N, P.K);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) x[a][j] = load16<ALIGNED>(P.x, t0 + 8 * j + g, k, P.T, P.K);
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                uint32_t wl[MT][2], wh[MT][2];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    widen4(word_of(w[a][i][0], f), wl[i][0], wh[i][0]);
+                    widen4(word_of(w[a][i][1], f), wl[i][1], wh[i][1]);
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    uint32_t xl, xh;
+                    widen4(word_of(x[a][j], f), xl, xh);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) mma_f16(acc[i][j], wl[i][0], wl[i][1], wh[i][0], wh[i][1], xl, xh);
+                }
+            }
+    }
+    // acc[i][j]: outputs 16 i + g and + 8, tokens 8 j + 2 q and + 1
+    float *mine = sums + warp * kTok * kPitch;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                mine[(8 * j + 2 * q + (c & 1)) * kPitch + 16 * i + g + 8 * (c >> 1)] = acc[i][j][c];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTok * kOut; i += 32 * kFewWarps) {
+        const uint64_t t = t0 + i / kOut, n = n0 + i % kOut;
+        if (t >= P.T || n >= P.N) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kFewWarps; ++s) v = __fadd_rn(v, sums[(s * kTok + i / kOut) * kPitch + i % kOut]);
+        v = __fmul_rn(v, __fmul_rn(__ldg(P.x_scale + t), __ldg(P.w_scale + n)));
+        if (P.bias) v = __fadd_rn(v, __ldg(P.bias + n));
+        if (P.y_bf16)
+            static_cast<uint16_t *>(P.y)[t * P.y_stride + n] = to_bf16(v);
+        else
+            static_cast<float *>(P.y)[t * P.y_stride + n] = v;
+    }
+}
+
+template <int NT, int MT, int AHEAD, bool ALIGNED>
+cudaError_t launch(const FewParams &p, cudaStream_t stream) {
+    const auto kernel = few_tokens<NT, MT, AHEAD, ALIGNED>;
+    constexpr size_t smem = sizeof(float) * kFewWarps * 8 * NT * (16 * MT + 1);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = prepare_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid(static_cast<unsigned>((p.N + 16 * MT - 1) / (16 * MT)),
+                    static_cast<unsigned>((p.T + 8 * NT - 1) / (8 * NT)));
+    kernel<<<grid, 32 * kFewWarps, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <bool ALIGNED>
+cudaError_t launch_for(const FewParams &p, cudaStream_t stream) {
+    if (p.T <= 8) return launch<1, 1, 8, ALIGNED>(p, stream);
+    if (p.T <= 16) return launch<2, 1, 4, ALIGNED>(p, stream);
+    if (p.T <= 32) return launch<4, 2, 2, ALIGNED>(p, stream);
+    return launch<8, 2, 1, ALIGNED>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_few(const ProductParams &p, cudaStream_t stream) {
+    const FewParams f{p.x_codes, p.w_codes, p.x_scale, p.w_scale, p.bias, p.T,
+                      p.N,       p.K,       p.out,     p.out_stride, p.out_bf16};
+    const bool aligned = p.K % 16 == 0 && ((reinterpret_cast<uintptr_t>(p.x_codes) | reinterpret_cast<uintptr_t>(p.w_codes)) & 15) == 0;
+    return aligned ? launch_for<true>(f, stream) : launch_for<false>(f, stream);
+}
+
+}  // namespace qc

@@ -478,14 +478,46 @@ cudaError_t launch_product(const Operand &a, const Operand &b, GemmParams g, voi
     return cudaGetLastError();
 }
 
-__global__ void column_sums(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t cols, float *out,
-                            int accumulate) {
-    const uint64_t c = static_cast<uint64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (c >= cols) return;
-    DWord s{0.0f, 0.0f};
-    for (uint64_t r = 0; r < rows; ++r) s = dw_add(s, bf16_bits_to_float(x[r * stride + c]));
-    const float v = __fadd_rn(s.hi, s.lo);
-    out[c] = accumulate ? __fadd_rn(out[c], v) : v;
+// Column sums of bf16 rows: a block owns 32 Q columns, lane l columns Q l .. Q l + Q - 1,
+// and its 32 warps every 32nd row; the warps' fp32 sums are added in order.
+template <int Q>
+__global__ void __launch_bounds__(1024) column_sums(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t cols,
+                                                    float *out, int accumulate) {
+    __shared__ float sums[32][32 * Q + 1];
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint64_t c = (static_cast<uint64_t>(blockIdx.x) * 32 + lane) * Q;
+    float s[Q] = {};
+    if (c < cols) {
+#pragma unroll 8
+        for (uint64_t r = warp; r < rows; r += 32) {
+            if constexpr (Q == 2) {
+                const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(x + r * stride + c));
+                s[0] = __fadd_rn(s[0], __uint_as_float(v << 16));
+                s[1] = __fadd_rn(s[1], __uint_as_float(v & 0xFFFF0000u));
+            } else {
+                s[0] = __fadd_rn(s[0], bf16_bits_to_float(__ldg(x + r * stride + c)));
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < Q; ++j) sums[warp][lane * Q + j] = s[j];
+    __syncthreads();
+    const uint64_t mine = static_cast<uint64_t>(blockIdx.x) * 32 * Q + threadIdx.x;
+    if (threadIdx.x < 32 * Q && mine < cols) {
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 32; ++w) v = __fadd_rn(v, sums[w][threadIdx.x]);
+        out[mine] = accumulate ? __fadd_rn(out[mine], v) : v;
+    }
+}
+
+cudaError_t launch_column_sums(const ProductParams &p, cudaStream_t stream) {
+    const bool pairs = p.N % 2 == 0 && p.dy_stride % 2 == 0 && (reinterpret_cast<uintptr_t>(p.dy) & 3) == 0;
+    const int cols = pairs ? 64 : 32;
+    const auto kernel = pairs ? column_sums<2> : column_sums<1>;
+    kernel<<<static_cast<unsigned>((p.N + cols - 1) / cols), 1024, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N, p.dbias,
+                                                                                p.accumulate);
+    return cudaGetLastError();
 }
 
 // Rows of 16-bit elements copied to rows that TMA can read.
@@ -538,7 +570,11 @@ GemmParams outputs(const ProductParams &p, uint64_t M, uint64_t N, uint64_t L) {
 
 }  // namespace
 
+// Up to this many tokens the weights are read as codes by qc_int8_few.cu.
+constexpr uint64_t kFewTokens = 128;
+
 size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K) {
+    if (T <= kFewTokens) return 0;
     return widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K);
 }
 size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
@@ -549,6 +585,7 @@ size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
 }
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
+    if (p.T <= kFewTokens) return launch_int8_few(p, stream);
     Operand x, w;
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     cudaError_t e = widen(p.x_codes, nullptr, p.T, p.K, ws, x, stream);
@@ -585,9 +622,7 @@ cudaError_t launch_int8_weight_grad(const ProductParams &p, cudaStream_t stream)
     if (e == cudaSuccess) e = launch_product<true, true>(dy, x, outputs(p, p.N, p.K, p.T),
                                        ws + widened_bytes(p.T, p.K) + widened_bytes(p.T, p.N), stream);
     if (e != cudaSuccess || !p.dbias) return e;
-    column_sums<<<static_cast<unsigned>((p.N + 127) / 128), 128, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N,
-                                                                              p.dbias, p.accumulate);
-    return cudaGetLastError();
+    return launch_column_sums(p, stream);
 }
 
 }  // namespace qc

@@ -350,6 +350,8 @@ size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K);
 size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K);
 size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K);
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream);
+// Few tokens: no workspace (qc_int8_few.cu).
+cudaError_t launch_int8_few(const ProductParams &p, cudaStream_t stream);
 cudaError_t launch_int8_input_grad(const ProductParams &p, cudaStream_t stream);
 cudaError_t launch_int8_weight_grad(const ProductParams &p, cudaStream_t stream);
 
