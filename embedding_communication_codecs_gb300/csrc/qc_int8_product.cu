@@ -52,7 +52,7 @@ struct Tile {
     static constexpr int kStages = BN == 256 ? 6 : 8;
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kWarpCols = BN / 2;               // columns of a storing warp
-    static constexpr int kTurn = kStoreWarps * 32 * 33 * 4;        // store_anywhere()
+    static constexpr int kTurn = kStoreWarps * 32 * 20 * 4;        // store_sums()
     static constexpr int kSmem = kStages * kStage + kTurn + 1024;  // tiles start on 1024 bytes
 };
 
@@ -95,71 +95,84 @@ __device__ __forceinline__ float finish(const GemmParams &P, uint64_t m, uint64_
     return P.bias ? __fadd_rn(v, __ldg(P.bias + n)) : v;
 }
 
-// A storing warp's C columns of row m (its lane's) from column n on, a vector at a
-// time: whole columns, rows on 16-byte boundaries.
-template <int C>
-__device__ __forceinline__ void store_vectors(const GemmParams &P, uint32_t split, uint64_t m, uint64_t n,
-                                              const float (&acc)[C]) {
-    if (P.splits > 1) {
-        float *o = P.partial + (split * P.M + m) * P.N + n;
-#pragma unroll
-        for (int c = 0; c < C; c += 4)
-            *reinterpret_cast<float4 *>(o + c) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
-    } else if (P.out_bf16) {
-        uint16_t *o = static_cast<uint16_t *>(P.out) + m * P.out_stride + n;
-#pragma unroll
-        for (int c = 0; c < C; c += 8) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = finish(P, m, n + c + j, acc[c + j]);
-            *reinterpret_cast<uint4 *>(o + c) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                           pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-        }
+// Where 16 columns of a warp's 32 rows are turned, so that its lanes store whole
+// 32-byte sectors: 20 floats a row keep 16-byte accesses free of bank conflicts.
+constexpr int kTurnCols = 16, kTurnPitch = 20;
+static_assert(Tile<256>::kTurn == kStoreWarps * 32 * kTurnPitch * 4, "room in the tile");
+
+// Four neighbouring results of row m from column n on, as fp32 or bf16.
+__device__ __forceinline__ void store4(const GemmParams &P, uint64_t m, uint64_t n, float4 v) {
+    if (P.out_bf16) {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + m * P.out_stride + n) =
+            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     } else {
-        float *o = static_cast<float *>(P.out) + m * P.out_stride + n;
-#pragma unroll
-        for (int c = 0; c < C; c += 4) {
-            float4 v = make_float4(finish(P, m, n + c, acc[c]), finish(P, m, n + c + 1, acc[c + 1]),
-                                   finish(P, m, n + c + 2, acc[c + 2]), finish(P, m, n + c + 3, acc[c + 3]));
-            if (P.accumulate) {
-                const float4 w = *reinterpret_cast<const float4 *>(o + c);
-                v = make_float4(__fadd_rn(w.x, v.x), __fadd_rn(w.y, v.y), __fadd_rn(w.z, v.z), __fadd_rn(w.w, v.w));
-            }
-            *reinterpret_cast<float4 *>(o + c) = v;
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(P.out) + m * P.out_stride + n);
+        if (P.accumulate) {
+            const float4 c = *o;
+            v = make_float4(__fadd_rn(c.x, v.x), __fadd_rn(c.y, v.y), __fadd_rn(c.z, v.z), __fadd_rn(c.w, v.w));
         }
+        *o = v;
     }
 }
 
-// The same at an edge of the matrix or where rows start anywhere: 32 x 32 sums are
-// turned in the warp's shared memory, so that its lanes store neighbouring columns
-// of one row.  m0 is the warp's first row.
+// A storing warp's C columns from n on of the 32 rows from m0 on (lane l holds row
+// m0 + l): scaled, biased and stored, or, of a split contraction, stored as they
+// are.  Four columns at a time inside the matrix where rows are on vector
+// boundaries (P.vector_out), single ones elsewhere.
 template <int C>
-__device__ __forceinline__ void store_anywhere(const GemmParams &P, uint32_t split, uint64_t m0, uint64_t n, int lane,
-                                               float (*turn)[33], const float (&acc)[C]) {
+__device__ __forceinline__ void store_sums(const GemmParams &P, uint32_t split, uint64_t m0, uint64_t n, int lane,
+                                           float (*turn)[kTurnPitch], const float (&acc)[C]) {
     const int rows = P.M - m0 < 32 ? static_cast<int>(P.M - m0) : 32;
 #pragma unroll
-    for (int c = 0; c < C; c += 32) {
+    for (int c = 0; c < C; c += kTurnCols) {
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) turn[lane][j] = acc[c + j];
+        for (int j = 0; j < kTurnCols; j += 4)
+            *reinterpret_cast<float4 *>(&turn[lane][j]) = make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
         __syncwarp();
-        const uint64_t col = n + c + lane;
-        if (col < P.N)
-            for (int r = 0; r < rows; ++r) {
-                const float sum = turn[r][lane];
+        if (P.vector_out && n + c + kTurnCols <= P.N) {
+            const uint64_t col = n + c + 4 * (lane & 3);
+            float4 ns = make_float4(1.0f, 1.0f, 1.0f, 1.0f), bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (P.m_scale) ns = make_float4(__ldg(P.n_scale + col), __ldg(P.n_scale + col + 1), __ldg(P.n_scale + col + 2), __ldg(P.n_scale + col + 3));
+            if (P.bias) bias = make_float4(__ldg(P.bias + col), __ldg(P.bias + col + 1), __ldg(P.bias + col + 2), __ldg(P.bias + col + 3));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + (lane >> 2);
+                if (r >= rows) continue;
                 const uint64_t m = m0 + r;
+                float4 v = *reinterpret_cast<const float4 *>(&turn[r][4 * (lane & 3)]);
                 if (P.splits > 1) {
-                    P.partial[(split * P.M + m) * P.N + col] = sum;
+                    *reinterpret_cast<float4 *>(P.partial + (split * P.M + m) * P.N + col) = v;
                     continue;
                 }
-                const float v = finish(P, m, col, sum);
-                if (P.out_bf16) {
-                    static_cast<uint16_t *>(P.out)[m * P.out_stride + col] = to_bf16(v);
-                } else {
-                    float *o = static_cast<float *>(P.out) + m * P.out_stride + col;
-                    *o = P.accumulate ? __fadd_rn(*o, v) : v;
+                if (P.m_scale) {
+                    const float ms = __ldg(P.m_scale + m);
+                    v = make_float4(__fmul_rn(v.x, __fmul_rn(ms, ns.x)), __fmul_rn(v.y, __fmul_rn(ms, ns.y)),
+                                    __fmul_rn(v.z, __fmul_rn(ms, ns.z)), __fmul_rn(v.w, __fmul_rn(ms, ns.w)));
                 }
+                if (P.bias)
+                    v = make_float4(__fadd_rn(v.x, bias.x), __fadd_rn(v.y, bias.y), __fadd_rn(v.z, bias.z), __fadd_rn(v.w, bias.w));
+                store4(P, m, col, v);
             }
+        } else {
+            const uint64_t col = n + c + (lane & 15);
+            if (col < P.N)
+                for (int r = lane >> 4; r < rows; r += 2) {
+                    const float sum = turn[r][lane & 15];
+                    const uint64_t m = m0 + r;
+                    if (P.splits > 1) {
+                        P.partial[(split * P.M + m) * P.N + col] = sum;
+                        continue;
+                    }
+                    const float v = finish(P, m, col, sum);
+                    if (P.out_bf16) {
+                        static_cast<uint16_t *>(P.out)[m * P.out_stride + col] = to_bf16(v);
+                    } else {
+                        float *o = static_cast<float *>(P.out) + m * P.out_stride + col;
+                        *o = P.accumulate ? __fadd_rn(*o, v) : v;
+                    }
+                }
+        }
     }
 }
 
@@ -172,7 +185,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     __shared__ uint64_t full[S], empty[S], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_slot;
     uint8_t *const tiles = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    float(*const turn)[32][33] = reinterpret_cast<float(*)[32][33]>(tiles + S * T::kStage);  // one per storing warp
+    float(*const turn)[32][kTurnPitch] =
+        reinterpret_cast<float(*)[32][kTurnPitch]>(tiles + S * T::kStage);  // one per storing warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t tiles_m = static_cast<uint32_t>((P.M + kPairM - 1) / kPairM);
@@ -309,10 +323,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const uint64_t m0 = static_cast<uint64_t>(w.m) * kPairM + rank * kBlockM + quarter * 32;
             const uint64_t n = static_cast<uint64_t>(w.n) * BN + c0;
             if (m0 >= P.M || n >= P.N) continue;
-            if (P.vector_out && m0 + 32 <= P.M && n + T::kWarpCols <= P.N)
-                store_vectors<T::kWarpCols>(P, w.split, m0 + lane, n, acc);
-            else
-                store_anywhere<T::kWarpCols>(P, w.split, m0, n, lane, turn[warp - 2], acc);
+            store_sums<T::kWarpCols>(P, w.split, m0, n, lane, turn[warp - 2], acc);
         }
     }
     if (!ok) report_failure(&g_product_error, P.status, kErrPipelineTimeout);
@@ -412,8 +423,9 @@ struct Plan {
 constexpr uint32_t kMaxSplits = 16;
 
 // The cheapest of a few cuts by an estimate in SM cycles: a pair goes through
-// ceil(units / pairs) units, each of its steps at 512 or 256 cycles (the tensor
-// core's rate for 256 x BN x 64) plus a start and a store of about 3000; a split one
+// ceil(units / pairs) units, each of its steps at 512 cycles (the tensor core's rate
+// for 256 x 256 x 64) or, for the narrower tile, hardly less (its loads bound it),
+// plus a start and a store of about 3000; a split one
 // also writes and reads its sums (about 2500 bytes a cycle) in a second launch.
 // `pairs` is fixed, so that the workspace's size does not depend on the device.
 Plan plan_for(uint64_t M, uint64_t N, uint64_t L) {
@@ -426,7 +438,7 @@ Plan plan_for(uint64_t M, uint64_t N, uint64_t L) {
         for (uint32_t s = 1; s <= kMaxSplits && (s == 1 || (steps / s >= 4 && tiles < kPairs)); ++s) {
             const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
             const uint64_t waves = (tiles * splits + kPairs - 1) / kPairs;
-            double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bn == 256 ? 512 : 280) + 3000);
+            double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bn == 256 ? 512 : 480) + 3000);
             if (splits > 1) cost += 6000 + static_cast<double>(splits) * M * N * 8 / 2500;
             if (cost < best_cost) {
                 best_cost = cost;
@@ -467,7 +479,7 @@ cudaError_t launch_product(const Operand &a, const Operand &b, GemmParams g, voi
     g.partial = static_cast<float *>(partial);
     const int esize = g.out_bf16 ? 2 : 4;
     g.vector_out = g.splits > 1 ? g.N % 4 == 0
-                                : (reinterpret_cast<uintptr_t>(g.out) & 15) == 0 && (g.out_stride * esize) % 16 == 0;
+                                : (reinterpret_cast<uintptr_t>(g.out) & (4 * esize - 1)) == 0 && g.out_stride % 4 == 0;
     const cudaError_t e = plan.bn == 256 ? launch_gemm<256, A_MN, B_MN>(a, b, g, stream)
                                          : launch_gemm<128, A_MN, B_MN>(a, b, g, stream);
     if (e != cudaSuccess || g.splits == 1) return e;

@@ -28,6 +28,29 @@ struct alignas(U * 2 > 16 ? 16 : U * 2) RawBf16 {
     uint16_t v[U];
     __device__ __forceinline__ float get(int j) const { return bf16_bits_to_float(v[j]); }
 };
+// The largest magnitude pattern of a unit, as an fp32 pattern.
+template <int U>
+__device__ __forceinline__ uint32_t unit_max(const RawF32<U> &r, uint32_t m) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) m = max(m, abs_bits(r.v[j]));
+    return m;
+}
+// bf16 patterns order like fp32 ones: pairs of them are compared at once.
+template <int U>
+__device__ __forceinline__ uint32_t unit_max(const RawBf16<U> &r, uint32_t m) {
+    if constexpr (U == 1) {
+        return max(m, (static_cast<uint32_t>(r.v[0]) & 0x7FFFu) << 16);
+    } else {
+        uint32_t p = 0;
+#pragma unroll
+        for (int j = 0; j < U; j += 2) {
+            const uint32_t w = static_cast<uint32_t>(r.v[j]) | static_cast<uint32_t>(r.v[j + 1]) << 16;
+            p = __vmaxu2(p, w & 0x7FFF7FFFu);
+        }
+        return max(m, max(p & 0xFFFF0000u, p << 16));
+    }
+}
+
 template <typename T, int U>
 struct RawOf;
 template <int U>
@@ -81,14 +104,9 @@ struct Team {
 // a row is enough; every thread of the block takes part.
 template <int N>
 __device__ __forceinline__ void team_max(uint32_t (&v)[N], uint32_t lanes, uint32_t (*red)[16][N], int &turn) {
-    if (lanes >= 32) {
+    for (uint32_t o = min(lanes, 32u) >> 1; o > 0; o >>= 1)
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = __reduce_max_sync(kFull, v[i]);
-    } else {
-        for (uint32_t o = lanes >> 1; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = max(v[i], __shfl_xor_sync(kFull, v[i], o));
-    }
+        for (int i = 0; i < N; ++i) v[i] = max(v[i], __shfl_xor_sync(kFull, v[i], o));
     if (lanes > 32) {
         const uint32_t warp = threadIdx.x >> 5, w0 = threadIdx.x / lanes * (lanes >> 5);
         if ((threadIdx.x & 31) == 0)
@@ -102,26 +120,34 @@ __device__ __forceinline__ void team_max(uint32_t (&v)[N], uint32_t lanes, uint3
     }
 }
 
-// Codes of U elements.  A row whose codes are all zero may hold infinities or NaN:
-// they are not multiplied.
+// Codes of U elements under a scale that neither zeroes nor saturates them.
 template <int U, typename Get>
-__device__ __forceinline__ void encode_unit(int8_t *out, const RowScale &s, Get get) {
+__device__ __forceinline__ void encode_unit(int8_t *out, float inverse, Get get) {
     uint32_t c[U];
-    if (s.inverse == 0.0f) {
 #pragma unroll
-        for (int j = 0; j < U; ++j) c[j] = 0u;
-    } else if (s.saturates) {
-#pragma unroll
-        for (int j = 0; j < U; ++j) c[j] = code_bits(clamp_to_cap(get(j)), s.inverse);
-    } else {
-#pragma unroll
-        for (int j = 0; j < U; ++j) c[j] = code_bits(get(j), s.inverse);
-    }
+    for (int j = 0; j < U; ++j) c[j] = code_bits(get(j), inverse);
     store_codes<U>(out, c);
 }
 
-template <typename T, int U, int V>
-__global__ void __launch_bounds__(kRowThreads) rows_encode(const RowCodesParams P, uint32_t lanes) {
+// The rare rows: all codes 0 (it may hold infinities and NaN, which are not
+// multiplied), or values to clamp.  Read again, a unit at a time, to keep their
+// code and registers out of the fast path.
+template <int U, typename Get>
+__device__ __noinline__ void encode_rare_row(int8_t *out, uint32_t units, uint32_t lane, uint32_t lanes, float inverse,
+                                             Get get) {
+#pragma unroll 1
+    for (uint32_t u = lane; u < units; u += lanes) {
+        uint32_t c[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) c[j] = inverse == 0.0f ? 0u : code_bits(clamp_to_cap(get(u * U + j)), inverse);
+        store_codes<U>(out + u * U, c);
+    }
+}
+
+// HELD: a team's lanes hold their row (units <= lanes * V); otherwise the second
+// pass reads it again.
+template <typename T, int U, int V, bool HELD, int BLOCKS>
+__global__ void __launch_bounds__(kRowThreads, BLOCKS) rows_encode(const RowCodesParams P, uint32_t lanes) {
     __shared__ uint32_t red[2][16][1];
     using R = typename RawOf<T, U>::type;
     const Team team(lanes);
@@ -131,38 +157,52 @@ __global__ void __launch_bounds__(kRowThreads) rows_encode(const RowCodesParams 
     for (uint64_t r0 = team.first - threadIdx.x / lanes; r0 < P.rows; r0 += team.stride) {
         const uint64_t r = r0 + threadIdx.x / lanes;
         const bool live = r < P.rows;
-        const T *x = static_cast<const T *>(P.x) + r * P.x_stride;
+        const T *x = static_cast<const T *>(P.x) + (live ? r : 0) * P.x_stride;
         R held[V];
         uint32_t m[1] = {0};
-        for (uint32_t base = 0; base < units; base += chunk) {
+        auto load = [&](uint32_t base) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const uint32_t u = base + v * lanes + team.lane;
-                if (live && u < units) held[v] = load_unit<T, U>(x + static_cast<uint64_t>(u) * U);
+                if (u < units) held[v] = load_unit<T, U>(x + u * U);
             }
+        };
+        auto largest = [&](uint32_t base) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const uint32_t u = base + v * lanes + team.lane;
-                if (live && u < units)
-#pragma unroll
-                    for (int j = 0; j < U; ++j) m[0] = max(m[0], abs_bits(held[v].get(j)));
+            for (int v = 0; v < V; ++v)
+                if (base + v * lanes + team.lane < units) m[0] = unit_max(held[v], m[0]);
+        };
+        if constexpr (HELD) {
+            load(0);
+            largest(0);
+        } else {
+            for (uint32_t base = 0; base < units; base += chunk) {
+                load(base);
+                largest(base);
             }
         }
         team_max(m, lanes, red, turn);
         const RowScale s = row_scale_of(m[0]);
         if (!live) continue;
         int8_t *out = P.codes + r * P.dim;
-        for (uint32_t base = 0; base < units; base += chunk) {
+        auto encode = [&](uint32_t base) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const uint32_t u = base + v * lanes + team.lane;
-                if (u < units) {
-                    const R h = units <= chunk ? held[v] : load_unit<T, U>(x + static_cast<uint64_t>(u) * U);
-                    encode_unit<U>(out + static_cast<uint64_t>(u) * U, s, [&](int j) { return h.get(j); });
-                }
+                if (u < units) encode_unit<U>(out + u * U, s.inverse, [&](int j) { return held[v].get(j); });
+            }
+        };
+        if (team.lane == 0) P.row_scale[r] = s.scale;
+        if (s.inverse == 0.0f || s.saturates) {
+            encode_rare_row<U>(out, units, team.lane, lanes, s.inverse, [=](uint32_t j) { return load_as_float(x + j); });
+        } else if constexpr (HELD) {
+            encode(0);
+        } else {
+            for (uint32_t base = 0; base < units; base += chunk) {
+                load(base);
+                encode(base);
             }
         }
-        if (team.lane == 0) P.row_scale[r] = s.scale;
     }
 }
 
@@ -220,8 +260,10 @@ __device__ __forceinline__ float sigmoid(float g) {
 
 __device__ __forceinline__ float swiglu(float g, float u) { return __fmul_rn(__fmul_rn(g, sigmoid(g)), u); }
 
-template <typename T, int U, int V, int THREADS>
-__global__ void __launch_bounds__(THREADS) swiglu_encode(const SwigluParams P, uint32_t lanes) {
+// HELD: h is held in registers between the two passes.  Gate and up are read again,
+// from L1 or L2: holding them too would leave one block to an SM.
+template <typename T, int U, int V, bool HELD, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) swiglu_encode(const SwigluParams P, uint32_t lanes) {
     __shared__ uint32_t red[2][16][3];
     using R = typename RawOf<T, U>::type;
     const Team team(lanes);
@@ -230,58 +272,70 @@ __global__ void __launch_bounds__(THREADS) swiglu_encode(const SwigluParams P, u
     for (uint64_t r0 = team.first - threadIdx.x / lanes; r0 < P.rows; r0 += team.stride) {
         const uint64_t r = r0 + threadIdx.x / lanes;
         const bool live = r < P.rows;
-        const T *gate = static_cast<const T *>(P.in) + r * P.in_stride, *up = gate + P.dim;
-        R g[V], w[V];
+        const T *gate = static_cast<const T *>(P.in) + (live ? r : 0) * P.in_stride, *up = gate + P.dim;
         float h[V][U];
         uint32_t m[3] = {0, 0, 0};
-        auto load = [&](uint32_t base) {
+        auto products = [&](uint32_t base) {
+            R g[V], w[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const uint32_t u = base + v * lanes + team.lane;
-                if (live && u < units) {
-                    g[v] = load_unit<T, U>(gate + static_cast<uint64_t>(u) * U);
-                    w[v] = load_unit<T, U>(up + static_cast<uint64_t>(u) * U);
+                if (u < units) {
+                    g[v] = load_unit<T, U>(gate + u * U);
+                    w[v] = load_unit<T, U>(up + u * U);
                 }
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (live && base + v * lanes + team.lane < units)
-#pragma unroll
-                    for (int j = 0; j < U; ++j) h[v][j] = swiglu(g[v].get(j), w[v].get(j));
-        };
-        for (uint32_t base = 0; base < units; base += chunk) {
-            load(base);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (live && base + v * lanes + team.lane < units)
+            for (int v = 0; v < V; ++v) {
+                if (base + v * lanes + team.lane < units) {
+                    m[0] = unit_max(g[v], m[0]);
+                    m[1] = unit_max(w[v], m[1]);
 #pragma unroll
                     for (int j = 0; j < U; ++j) {
-                        m[0] = max(m[0], abs_bits(g[v].get(j)));
-                        m[1] = max(m[1], abs_bits(w[v].get(j)));
+                        h[v][j] = swiglu(g[v].get(j), w[v].get(j));
                         m[2] = max(m[2], abs_bits(h[v][j]));
                     }
+                }
+            }
+        };
+        if constexpr (HELD) {
+            products(0);
+        } else {
+            for (uint32_t base = 0; base < units; base += chunk) products(base);
         }
         team_max(m, lanes, red, turn);
         const RowScale sg = row_scale_of(m[0]), su = row_scale_of(m[1]), sh = row_scale_of(m[2]);
         if (!live) continue;
         int8_t *saved = P.saved_codes + r * 2 * P.dim, *out = P.h_codes + r * P.dim;
-        for (uint32_t base = 0; base < units; base += chunk) {
-            if (units > chunk) load(base);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const uint32_t u = base + v * lanes + team.lane;
-                if (u < units) {
-                    const uint64_t at = static_cast<uint64_t>(u) * U;
-                    encode_unit<U>(saved + at, sg, [&](int j) { return g[v].get(j); });
-                    encode_unit<U>(saved + P.dim + at, su, [&](int j) { return w[v].get(j); });
-                    encode_unit<U>(out + at, sh, [&](int j) { return h[v][j]; });
-                }
-            }
-        }
         if (team.lane == 0) {
             P.saved_scale[2 * r] = sg.scale;
             P.saved_scale[2 * r + 1] = su.scale;
             P.h_scale[r] = sh.scale;
+        }
+        auto encode = [&](uint32_t base) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t u = base + v * lanes + team.lane;
+                if (u < units) {
+                    const R g = load_unit<T, U>(gate + u * U), w = load_unit<T, U>(up + u * U);
+                    encode_unit<U>(saved + u * U, sg.inverse, [&](int j) { return g.get(j); });
+                    encode_unit<U>(saved + P.dim + u * U, su.inverse, [&](int j) { return w.get(j); });
+                    encode_unit<U>(out + u * U, sh.inverse, [&](int j) { return h[v][j]; });
+                }
+            }
+        };
+        if (sg.inverse == 0.0f || su.inverse == 0.0f || sh.inverse == 0.0f || sg.saturates || su.saturates || sh.saturates) {
+            encode_rare_row<U>(saved, units, team.lane, lanes, sg.inverse, [=](uint32_t j) { return load_as_float(gate + j); });
+            encode_rare_row<U>(saved + P.dim, units, team.lane, lanes, su.inverse, [=](uint32_t j) { return load_as_float(up + j); });
+            encode_rare_row<U>(out, units, team.lane, lanes, sh.inverse,
+                               [=](uint32_t j) { return swiglu(load_as_float(gate + j), load_as_float(up + j)); });
+        } else if constexpr (HELD) {
+            encode(0);
+        } else {
+            for (uint32_t base = 0; base < units; base += chunk) {
+                products(base);
+                encode(base);
+            }
         }
     }
 }
@@ -351,15 +405,19 @@ bool fits(const void *p, uint64_t stride, size_t esize, uint32_t dim, uint32_t u
 
 template <typename T>
 cudaError_t encode_rows(const RowCodesParams &p, cudaStream_t stream) {
+    constexpr bool kWide = sizeof(T) == 4;  // fp32 units take twice the registers
     const uint32_t d = p.dim;
     if (!fits(p.x, p.x_stride, sizeof(T), d, 8, 16) || !fits(p.codes, d, 1, d, 8, 8)) {
-        if (d <= 8 * kRowThreads) return launch_rows(rows_encode<T, 1, 8>, p, lanes_for(d, 8, kRowThreads), kRowThreads, stream);
-        return launch_rows(rows_encode<T, 1, 32>, p, kRowThreads, kRowThreads, stream);
+        if (d <= 8 * kRowThreads) return launch_rows(rows_encode<T, 1, 8, true, 6>, p, lanes_for(d, 8, kRowThreads), kRowThreads, stream);
+        if (d <= 32 * kRowThreads) return launch_rows(rows_encode<T, 1, 32, true, 3>, p, kRowThreads, kRowThreads, stream);
+        return launch_rows(rows_encode<T, 1, 8, false, 6>, p, kRowThreads, kRowThreads, stream);
     }
     const uint32_t units = d / 8;
-    if (units <= 32) return launch_rows(rows_encode<T, 8, 1>, p, lanes_for(units, 1, 32), kRowThreads, stream);
-    if (units <= 4 * kRowThreads) return launch_rows(rows_encode<T, 8, 4>, p, lanes_for(units, 4, kRowThreads), kRowThreads, stream);
-    return launch_rows(rows_encode<T, 8, 8>, p, kRowThreads, kRowThreads, stream);
+    if (units <= 32) return launch_rows(rows_encode<T, 8, 1, true, 8>, p, lanes_for(units, 1, 32), kRowThreads, stream);
+    if (units <= 4 * kRowThreads)
+        return launch_rows(rows_encode<T, 8, 4, true, kWide ? 4 : 6>, p, lanes_for(units, 4, kRowThreads), kRowThreads, stream);
+    if (units <= 8 * kRowThreads) return launch_rows(rows_encode<T, 8, 8, true, kWide ? 2 : 3>, p, kRowThreads, kRowThreads, stream);
+    return launch_rows(rows_encode<T, 8, 4, false, 4>, p, kRowThreads, kRowThreads, stream);
 }
 
 template <typename T>
@@ -378,11 +436,16 @@ cudaError_t encode_swiglu(const SwigluParams &p, cudaStream_t stream) {
     // the ups start dim elements into a row: dim % 8 == 0 aligns them as the gates
     if (!fits(p.in, p.in_stride, sizeof(T), d, 8, 16) || !fits(p.h_codes, d, 1, d, 8, 8) ||
         !fits(p.saved_codes, 2 * d, 1, d, 8, 8))
-        return launch_rows(swiglu_encode<T, 1, 8, 512>, p, lanes_for(d, 8, 512), 512, stream);
+        return d <= 8 * 512 ? launch_rows(swiglu_encode<T, 1, 8, true, 512, 2>, p, lanes_for(d, 8, 512), 512, stream)
+                            : launch_rows(swiglu_encode<T, 1, 4, false, 512, 2>, p, 512, 512, stream);
     const uint32_t units = d / 8;
-    if (units <= 64) return launch_rows(swiglu_encode<T, 8, 1, 256>, p, lanes_for(units, 1, 64), 256, stream);
-    if (units <= 1024) return launch_rows(swiglu_encode<T, 8, 2, 512>, p, lanes_for(units, 2, 512), 512, stream);
-    return launch_rows(swiglu_encode<T, 8, 4, 512>, p, 512, 512, stream);
+    // blocks to an SM as the registers allow without spills
+    constexpr bool kWide = sizeof(T) == 4;
+    if (units <= 512)
+        return launch_rows(swiglu_encode<T, 8, 2, true, 256, kWide ? 3 : 4>, p, lanes_for(units, 2, 256), 256, stream);
+    if (units <= 2048)
+        return launch_rows(swiglu_encode<T, 8, 4, true, 512, 1>, p, lanes_for(units, 4, 512), 512, stream);
+    return launch_rows(swiglu_encode<T, 8, 1, false, 256, 3>, p, 256, 256, stream);
 }
 
 template <typename T>
