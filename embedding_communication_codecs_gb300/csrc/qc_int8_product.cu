@@ -52,17 +52,17 @@ struct Tile {
     static constexpr int kStages = BN == 256 ? 6 : 8;
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kWarpCols = BN / 2;               // columns of a storing warp
-    static constexpr int kTurn = kStoreWarps * 32 * 20 * 4;        // store_sums()
-    static constexpr int kSmem = kStages * kStage + kTurn + 1024;  // tiles start on 1024 bytes
+    static constexpr int kSmem = kStages * kStage + kStoreWarps * 4096 + 1024;  // tiles start on 1024 bytes
 };
 
 struct GemmParams {
     uint64_t M, N, L;
     uint32_t splits, split_steps;  // the contraction in `splits` ranges of split_steps steps
-    float *partial;                // splits x M x N sums, where splits > 1
+    float *partial;                // where splits > 1: splits x ceil32(M) rows of partial_pitch sums
+    uint64_t partial_pitch;
     void *out;
     uint64_t out_stride;
-    int out_bf16, accumulate, vector_out;
+    int out_bf16, accumulate;
     const float *m_scale, *n_scale, *bias;
     uint32_t *status;
 };
@@ -95,98 +95,135 @@ __device__ __forceinline__ float finish(const GemmParams &P, uint64_t m, uint64_
     return P.bias ? __fadd_rn(v, __ldg(P.bias + n)) : v;
 }
 
-// Where 16 columns of a warp's 32 rows are turned, so that its lanes store whole
-// 32-byte sectors: 20 floats a row keep 16-byte accesses free of bank conflicts.
-constexpr int kTurnCols = 16, kTurnPitch = 20;
-static_assert(Tile<256>::kTurn == kStoreWarps * 32 * kTurnPitch * 4, "room in the tile");
-
-// Four neighbouring results of row m from column n on, as fp32 or bf16.
-__device__ __forceinline__ void store4(const GemmParams &P, uint64_t m, uint64_t n, float4 v) {
-    if (P.out_bf16) {
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + m * P.out_stride + n) =
-            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-    } else {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(P.out) + m * P.out_stride + n);
-        if (P.accumulate) {
-            const float4 c = *o;
-            v = make_float4(__fadd_rn(c.x, v.x), __fadd_rn(c.y, v.y), __fadd_rn(c.z, v.z), __fadd_rn(c.w, v.w));
-        }
-        *o = v;
+// Adds a storing warp's C columns of tensor memory to its registers.
+template <int C>
+__device__ __forceinline__ void add_sums(uint32_t at, float (&acc)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; c += 8) {
+        uint32_t v[8];
+        tmem_load8(at + c, v);
+        tmem_wait_load();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[c + j] = __fadd_rn(acc[c + j], __uint_as_float(v[j]));
     }
+}
+
+// How a kernel writes its results.
+enum Output : int {
+    kSums,       // fp32 sums of a split contraction, by TMA
+    kF32,        // fp32 results, by TMA
+    kF32Add,     // added to what is there, by TMA
+    kBf16,       // bf16 results, by TMA
+    kAnywhere    // rows that TMA cannot write (not on 16-byte boundaries), element by element
+};
+
+// Byte offset of 16-byte piece `i` of row `r` in a warp's 32 rows of 128 bytes, as the
+// 128-byte swizzle lays them out; pieces i of 8 neighbouring rows share no bank.
+__device__ __forceinline__ uint32_t swizzled(int r, int i) { return r * 128 + ((i ^ (r & 7)) << 4); }
+
+// A scale or bias, loaded where it stands: hoisted above the stores, these loads'
+// registers would push sums into local memory.
+__device__ __forceinline__ float load_here(const float *p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
+// Four sums of columns n .. n + 3 scaled and biased (the columns past the last are
+// not stored; their scales are read from the last one).
+__device__ __forceinline__ float4 finish4(const GemmParams &P, float ms, uint32_t n, const float *v) {
+    float r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t c = min(n + j, static_cast<uint32_t>(P.N) - 1);
+        r[j] = v[j];
+        if (P.m_scale) r[j] = __fmul_rn(r[j], __fmul_rn(ms, load_here(P.n_scale + c)));
+        if (P.bias) r[j] = __fadd_rn(r[j], load_here(P.bias + c));
+    }
+    return make_float4(r[0], r[1], r[2], r[3]);
 }
 
 // A storing warp's C columns from n on of the 32 rows from m0 on (lane l holds row
-// m0 + l): scaled, biased and stored, or, of a split contraction, stored as they
-// are.  Four columns at a time inside the matrix where rows are on vector
-// boundaries (P.vector_out), single ones elsewhere.
-template <int C>
-__device__ __forceinline__ void store_sums(const GemmParams &P, uint32_t split, uint64_t m0, uint64_t n, int lane,
-                                           float (*turn)[kTurnPitch], const float (&acc)[C]) {
-    const int rows = P.M - m0 < 32 ? static_cast<int>(P.M - m0) : 32;
+// m0 + l): scaled, biased, written to the warp's 4 KB of shared memory as 32 rows of
+// 128 bytes and stored from there by TMA.
+template <int C, Output OUT>
+__device__ __forceinline__ void store_tma(const GemmParams &P, const CUtensorMap &map, uint32_t split, uint32_t m0,
+                                          uint32_t n, int lane, uint8_t *buf, const float (&acc)[C]) {
+    constexpr int kCols = OUT == kBf16 ? 64 : 32;
+    const float ms = OUT != kSums && P.m_scale ? __ldg(P.m_scale + (m0 + lane < P.M ? m0 + lane : P.M - 1)) : 1.0f;
+    const int y = static_cast<int>(OUT == kSums ? split * ((static_cast<uint32_t>(P.M) + 31) / 32 * 32) + m0 : m0);
 #pragma unroll
-    for (int c = 0; c < C; c += kTurnCols) {
+    for (int c = 0; c < C; c += kCols) {
+        if (n + c >= P.N) break;
+        if (lane == 0) tma_store_wait_read();
         __syncwarp();
 #pragma unroll
-        for (int j = 0; j < kTurnCols; j += 4)
-            *reinterpret_cast<float4 *>(&turn[lane][j]) = make_float4(acc[c + j], acc[c + j + 1], acc[c + j + 2], acc[c + j + 3]);
-        __syncwarp();
-        if (P.vector_out && n + c + kTurnCols <= P.N) {
-            const uint64_t col = n + c + 4 * (lane & 3);
-            float4 ns = make_float4(1.0f, 1.0f, 1.0f, 1.0f), bias = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (P.m_scale) ns = make_float4(__ldg(P.n_scale + col), __ldg(P.n_scale + col + 1), __ldg(P.n_scale + col + 2), __ldg(P.n_scale + col + 3));
-            if (P.bias) bias = make_float4(__ldg(P.bias + col), __ldg(P.bias + col + 1), __ldg(P.bias + col + 2), __ldg(P.bias + col + 3));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 8 * i + (lane >> 2);
-                if (r >= rows) continue;
-                const uint64_t m = m0 + r;
-                float4 v = *reinterpret_cast<const float4 *>(&turn[r][4 * (lane & 3)]);
-                if (P.splits > 1) {
-                    *reinterpret_cast<float4 *>(P.partial + (split * P.M + m) * P.N + col) = v;
-                    continue;
-                }
-                if (P.m_scale) {
-                    const float ms = __ldg(P.m_scale + m);
-                    v = make_float4(__fmul_rn(v.x, __fmul_rn(ms, ns.x)), __fmul_rn(v.y, __fmul_rn(ms, ns.y)),
-                                    __fmul_rn(v.z, __fmul_rn(ms, ns.z)), __fmul_rn(v.w, __fmul_rn(ms, ns.w)));
-                }
-                if (P.bias)
-                    v = make_float4(__fadd_rn(v.x, bias.x), __fadd_rn(v.y, bias.y), __fadd_rn(v.z, bias.z), __fadd_rn(v.w, bias.w));
-                store4(P, m, col, v);
+        for (int i = 0; i < 8; ++i) {
+            uint4 w;
+            if constexpr (OUT == kBf16) {
+                const float4 lo = finish4(P, ms, n + c + 8 * i, acc + c + 8 * i), hi = finish4(P, ms, n + c + 8 * i + 4, acc + c + 8 * i + 4);
+                w = make_uint4(pack_bf16(lo.x, lo.y), pack_bf16(lo.z, lo.w), pack_bf16(hi.x, hi.y), pack_bf16(hi.z, hi.w));
+            } else {
+                float4 v = make_float4(acc[c + 4 * i], acc[c + 4 * i + 1], acc[c + 4 * i + 2], acc[c + 4 * i + 3]);
+                if constexpr (OUT != kSums) v = finish4(P, ms, n + c + 4 * i, acc + c + 4 * i);
+                w = make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w));
             }
-        } else {
-            const uint64_t col = n + c + (lane & 15);
-            if (col < P.N)
-                for (int r = lane >> 4; r < rows; r += 2) {
-                    const float sum = turn[r][lane & 15];
-                    const uint64_t m = m0 + r;
-                    if (P.splits > 1) {
-                        P.partial[(split * P.M + m) * P.N + col] = sum;
-                        continue;
-                    }
-                    const float v = finish(P, m, col, sum);
-                    if (P.out_bf16) {
-                        static_cast<uint16_t *>(P.out)[m * P.out_stride + col] = to_bf16(v);
-                    } else {
-                        float *o = static_cast<float *>(P.out) + m * P.out_stride + col;
-                        *o = P.accumulate ? __fadd_rn(*o, v) : v;
-                    }
-                }
+            *reinterpret_cast<uint4 *>(buf + swizzled(lane, i)) = w;
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store<OUT == kF32Add>(&map, static_cast<int>(n + c), y, buf);
+            tma_store_commit();
         }
     }
 }
 
-template <int BN, bool A_MN, bool B_MN>
+// The same, element by element: 32 x 32 sums through the warp's shared memory, so
+// that its lanes store neighbouring columns of one row.
+template <int C>
+__device__ __forceinline__ void store_anywhere(const GemmParams &P, uint32_t m0, uint32_t n, int lane, uint8_t *buf,
+                                               const float (&acc)[C]) {
+    const int rows = P.M - m0 < 32 ? static_cast<int>(P.M - m0) : 32;
+#pragma unroll
+    for (int c = 0; c < C; c += 32) {
+        if (n + c >= P.N) break;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4 *>(buf + swizzled(lane, i)) =
+                make_float4(acc[c + 4 * i], acc[c + 4 * i + 1], acc[c + 4 * i + 2], acc[c + 4 * i + 3]);
+        __syncwarp();
+        const uint32_t col = n + c + lane;
+        if (col < P.N) {
+            const float ns = P.m_scale ? __ldg(P.n_scale + col) : 1.0f, bias = P.bias ? __ldg(P.bias + col) : 0.0f;
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+                float v = *reinterpret_cast<const float *>(buf + swizzled(r, lane >> 2) + 4 * (lane & 3));
+                if (P.m_scale) v = __fmul_rn(v, __fmul_rn(__ldg(P.m_scale + m0 + r), ns));
+                if (P.bias) v = __fadd_rn(v, bias);
+                const uint64_t at = static_cast<uint64_t>(m0 + r) * P.out_stride + col;
+                if (P.out_bf16) {
+                    static_cast<uint16_t *>(P.out)[at] = to_bf16(v);
+                } else {
+                    float *o = static_cast<float *>(P.out) + at;
+                    *o = P.accumulate ? __fadd_rn(*o, v) : v;
+                }
+            }
+        }
+    }
+}
+
+template <int BN, bool A_MN, bool B_MN, Output OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
-    gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemmParams P) {
+    gemm(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+         const __grid_constant__ CUtensorMap map_out, const GemmParams P) {
     using T = Tile<BN>;
     constexpr int S = T::kStages;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[S], empty[S], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_slot;
     uint8_t *const tiles = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    float(*const turn)[32][kTurnPitch] =
-        reinterpret_cast<float(*)[32][kTurnPitch]>(tiles + S * T::kStage);  // one per storing warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t tiles_m = static_cast<uint32_t>((P.M + kPairM - 1) / kPairM);
@@ -294,37 +331,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int quarter = warp & 3;                         // the 32 lanes of tensor memory that this warp may read
         const uint32_t c0 = (warp - 2) / 4 * T::kWarpCols;    // its half of the columns
         const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+        uint8_t *const buf = tiles + S * T::kStage + (warp - 2) * 4096;
         uint32_t part = 0;
         for (uint32_t u = pair; u < units && ok; u += npairs) {
-            const Unit w = unit_at(u, tiles_m, tiles_n, P);
-            float acc[T::kWarpCols];
-            for (uint32_t k0 = 0; k0 < w.steps; k0 += kPartSteps, ++part) {
-                const uint32_t buf = part & 1;
-                ok = mbar_wait_cluster(&sums_full[buf], (part >> 1) & 1);
+            float acc[T::kWarpCols] = {};
+            const uint32_t parts = (unit_at(u, tiles_m, tiles_n, P).steps + kPartSteps - 1) / kPartSteps;
+            for (uint32_t left = parts; left > 0; --left, ++part) {
+                ok = mbar_wait_cluster(&sums_full[part & 1], (part >> 1) & 1);
                 if (__any_sync(kFull, !ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < T::kWarpCols; c += 16) {
-                    uint32_t v[16];
-                    tmem_load16(from + buf * BN + c, v);
-                    tmem_wait_load();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[c + j] = k0 == 0 ? __uint_as_float(v[j]) : __fadd_rn(acc[c + j], __uint_as_float(v[j]));
-                }
+                add_sums(from + (part & 1) * BN, acc);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(in_block(&sums_empty[buf], 0));
+                if (lane == 0) mbar_arrive_cluster(in_block(&sums_empty[part & 1], 0));
             }
             if (!ok) break;
-            const uint64_t m0 = static_cast<uint64_t>(w.m) * kPairM + rank * kBlockM + quarter * 32;
-            const uint64_t n = static_cast<uint64_t>(w.n) * BN + c0;
+            const Unit w = unit_at(u, tiles_m, tiles_n, P);
+            const uint32_t m0 = w.m * kPairM + rank * kBlockM + quarter * 32, n = w.n * BN + c0;
             if (m0 >= P.M || n >= P.N) continue;
-            store_sums<T::kWarpCols>(P, w.split, m0, n, lane, turn[warp - 2], acc);
+            if constexpr (OUT == kAnywhere)
+                store_anywhere<T::kWarpCols>(P, m0, n, lane, buf, acc);
+            else
+                store_tma<T::kWarpCols, OUT>(P, map_out, w.split, m0, n, lane, buf, acc);
         }
+        if (lane == 0) tma_store_wait_read();  // the block's shared memory outlives the stores' reads
     }
     if (!ok) report_failure(&g_product_error, P.status, kErrPipelineTimeout);
     tc_fence_before();
@@ -333,27 +366,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (warp == 1) tmem_free_pair<T::kTmemCols>(tmem);
 }
 
-// The ranges of a split contraction, added in order: Q columns of a row per thread.
-template <int Q>
+// The ranges of a split contraction, added in order: four columns of a row per thread.
 __global__ void __launch_bounds__(256) join(const GemmParams P) {
-    const uint64_t per_row = P.N / Q, total = P.M * per_row;
+    const uint64_t per_row = (P.N + 3) / 4, total = P.M * per_row, rows = (P.M + 31) / 32 * 32;
     for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<uint64_t>(gridDim.x) * 256) {
-        const uint64_t m = i / per_row, n = i % per_row * Q;
-        float v[Q] = {};
+        const uint64_t m = i / per_row, n = i % per_row * 4;
+        float v[4] = {};
         for (uint32_t s = 0; s < P.splits; ++s) {
-            const float *p = P.partial + (s * P.M + m) * P.N + n;
-            if constexpr (Q == 4) {
-                const float4 w = *reinterpret_cast<const float4 *>(p);
-                v[0] = __fadd_rn(v[0], w.x);
-                v[1] = __fadd_rn(v[1], w.y);
-                v[2] = __fadd_rn(v[2], w.z);
-                v[3] = __fadd_rn(v[3], w.w);
-            } else {
-                v[0] = __fadd_rn(v[0], *p);
-            }
+            const float4 w = *reinterpret_cast<const float4 *>(P.partial + (s * rows + m) * P.partial_pitch + n);
+            v[0] = __fadd_rn(v[0], w.x);
+            v[1] = __fadd_rn(v[1], w.y);
+            v[2] = __fadd_rn(v[2], w.z);
+            v[3] = __fadd_rn(v[3], w.w);
         }
 #pragma unroll
-        for (int j = 0; j < Q; ++j) {
+        for (int j = 0; j < 4; ++j) {
+            if (n + j >= P.N) break;
             const float r = finish(P, m, n + j, v[j]);
             if (P.out_bf16) {
                 static_cast<uint16_t *>(P.out)[m * P.out_stride + n + j] = to_bf16(r);
@@ -383,14 +411,16 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// A matrix of 16-bit elements, `rows` rows of `dim` elements `stride` apart, as
-// boxes of box_rows x 64 under the 128-byte swizzle; zeros outside.
-bool make_map(CUtensorMap *map, const void *p, uint64_t rows, uint64_t dim, uint64_t stride, uint32_t box_rows) {
-    const cuuint64_t dims[2] = {dim, rows}, strides[1] = {stride * 2};
-    const cuuint32_t box[2] = {64, box_rows}, unit[2] = {1, 1};
+// `rows` rows of `dim` elements `stride` apart, as boxes of box_rows rows of 128
+// bytes under the 128-byte swizzle; reads outside give zeros, writes are dropped.
+bool make_map(CUtensorMap *map, const void *p, bool bf16, uint64_t rows, uint64_t dim, uint64_t stride, uint32_t box_rows) {
+    const uint32_t esize = bf16 ? 2 : 4;
+    const cuuint64_t dims[2] = {dim, rows}, strides[1] = {stride * esize};
+    const cuuint32_t box[2] = {128 / esize, box_rows}, unit[2] = {1, 1};
     EncodeTiled fn = encode_tiled();
-    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, unit,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return fn && fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                    const_cast<void *>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -400,8 +430,8 @@ struct Operand {
     uint64_t rows, dim, stride;
 };
 
-bool tma_fits(const void *p, uint64_t stride) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0;
+bool tma_fits(const void *p, uint64_t stride, size_t esize) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * esize % 16 == 0;
 }
 
 int sm_count() {
@@ -449,45 +479,58 @@ Plan plan_for(uint64_t M, uint64_t N, uint64_t L) {
     return best;
 }
 
+// Sums of a split contraction: rows and row pitch in whole 32s.
+uint64_t ceil32(uint64_t v) { return (v + 31) / 32 * 32; }
 uint64_t partial_bytes(uint64_t M, uint64_t N, uint64_t L) {
     const Plan p = plan_for(M, N, L);
-    return p.splits > 1 ? (p.splits * M * N * 4 + 255) / 256 * 256 : 0;
+    return p.splits > 1 ? p.splits * ceil32(M) * ceil32(N) * 4 : 0;
 }
 
-template <int BN, bool A_MN, bool B_MN>
+template <int BN, bool A_MN, bool B_MN, Output OUT>
 cudaError_t launch_gemm(const Operand &a, const Operand &b, const GemmParams &g, cudaStream_t stream) {
     using T = Tile<BN>;
-    const auto kernel = gemm<BN, A_MN, B_MN>;
-    CUtensorMap ma, mb;
-    if (!make_map(&ma, a.p, a.rows, a.dim, a.stride, A_MN ? kStep : kBlockM) ||
-        !make_map(&mb, b.p, b.rows, b.dim, b.stride, B_MN ? kStep : T::kRowsB))
-        return cudaErrorInvalidValue;
+    const auto kernel = gemm<BN, A_MN, B_MN, OUT>;
+    CUtensorMap ma, mb, mo{};
+    bool mapped = make_map(&ma, a.p, true, a.rows, a.dim, a.stride, A_MN ? kStep : kBlockM) &&
+                  make_map(&mb, b.p, true, b.rows, b.dim, b.stride, B_MN ? kStep : T::kRowsB);
+    if (OUT == kSums) mapped = mapped && make_map(&mo, g.partial, false, g.splits * ceil32(g.M), g.N, g.partial_pitch, 32);
+    if (OUT == kF32 || OUT == kF32Add || OUT == kBf16) mapped = mapped && make_map(&mo, g.out, OUT == kBf16, g.M, g.N, g.out_stride, 32);
+    if (!mapped) return cudaErrorInvalidValue;
     cudaError_t e = prepare_dynamic_smem(reinterpret_cast<const void *>(kernel), T::kSmem);
     if (e != cudaSuccess) return e;
     const uint64_t units = ((g.M + kPairM - 1) / kPairM) * ((g.N + BN - 1) / BN) * g.splits;
     if (units > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
     const uint64_t most = sm_count() / 2;  // one block per SM, in pairs
-    kernel<<<static_cast<unsigned>(2 * (units < most ? units : most)), kGemmThreads, T::kSmem, stream>>>(ma, mb, g);
+    kernel<<<static_cast<unsigned>(2 * (units < most ? units : most)), kGemmThreads, T::kSmem, stream>>>(ma, mb, mo, g);
     return cudaGetLastError();
 }
 
-template <bool A_MN, bool B_MN>
+template <bool A_MN, bool B_MN, Output OUT>
+cudaError_t launch_tile(int bn, const Operand &a, const Operand &b, const GemmParams &g, cudaStream_t stream) {
+    return bn == 256 ? launch_gemm<256, A_MN, B_MN, OUT>(a, b, g, stream) : launch_gemm<128, A_MN, B_MN, OUT>(a, b, g, stream);
+}
+
+// ADDS: this product may accumulate.
+template <bool A_MN, bool B_MN, bool ADDS>
 cudaError_t launch_product(const Operand &a, const Operand &b, GemmParams g, void *partial, cudaStream_t stream) {
     const Plan plan = plan_for(g.M, g.N, g.L);
     g.splits = plan.splits;
     g.split_steps = plan.split_steps;
     g.partial = static_cast<float *>(partial);
-    const int esize = g.out_bf16 ? 2 : 4;
-    g.vector_out = g.splits > 1 ? g.N % 4 == 0
-                                : (reinterpret_cast<uintptr_t>(g.out) & (4 * esize - 1)) == 0 && g.out_stride % 4 == 0;
-    const cudaError_t e = plan.bn == 256 ? launch_gemm<256, A_MN, B_MN>(a, b, g, stream)
-                                         : launch_gemm<128, A_MN, B_MN>(a, b, g, stream);
-    if (e != cudaSuccess || g.splits == 1) return e;
-    const auto kernel = g.N % 4 == 0 ? join<4> : join<1>;
-    const uint64_t work = g.M * (g.N % 4 == 0 ? g.N / 4 : g.N);
-    const int grid = persistent_grid(reinterpret_cast<const void *>(kernel), 256, (work + 255) / 256);
-    kernel<<<grid, 256, 0, stream>>>(g);
-    return cudaGetLastError();
+    g.partial_pitch = ceil32(g.N);
+    if (g.splits > 1) {
+        const cudaError_t e = launch_tile<A_MN, B_MN, kSums>(plan.bn, a, b, g, stream);
+        if (e != cudaSuccess) return e;
+        const uint64_t work = g.M * ((g.N + 3) / 4);
+        const int grid = persistent_grid(reinterpret_cast<const void *>(&join), 256, (work + 255) / 256);
+        join<<<grid, 256, 0, stream>>>(g);
+        return cudaGetLastError();
+    }
+    if (!tma_fits(g.out, g.out_stride, g.out_bf16 ? 2 : 4)) return launch_tile<A_MN, B_MN, kAnywhere>(plan.bn, a, b, g, stream);
+    if (g.out_bf16) return launch_tile<A_MN, B_MN, kBf16>(plan.bn, a, b, g, stream);
+    if constexpr (ADDS)
+        if (g.accumulate) return launch_tile<A_MN, B_MN, kF32Add>(plan.bn, a, b, g, stream);
+    return launch_tile<A_MN, B_MN, kF32>(plan.bn, a, b, g, stream);
 }
 
 // Column sums of bf16 rows: a block owns 32 Q columns, lane l columns Q l .. Q l + Q - 1,
@@ -560,7 +603,7 @@ cudaError_t widen(const int8_t *codes, const float *scale, uint64_t rows, uint64
 // dy as TMA can read it: in place, or copied to the workspace.
 cudaError_t readable_dy(const ProductParams &p, void *room, Operand &op, cudaStream_t stream) {
     op = {p.dy, p.T, p.N, p.dy_stride};
-    if (tma_fits(p.dy, p.dy_stride)) return cudaSuccess;
+    if (tma_fits(p.dy, p.dy_stride, 2)) return cudaSuccess;
     op = {room, p.T, p.N, padded(p.N)};
     const int grid = persistent_grid(reinterpret_cast<const void *>(&copy_rows), 256, p.T);
     copy_rows<<<grid, 256, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N, static_cast<uint16_t *>(room), padded(p.N));
@@ -607,7 +650,7 @@ cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
     g.m_scale = p.x_scale;
     g.n_scale = p.w_scale;
     g.bias = p.bias;
-    return launch_product<false, false>(x, w, g, ws + widened_bytes(p.T, p.K) + widened_bytes(p.N, p.K), stream);
+    return launch_product<false, false, false>(x, w, g, ws + widened_bytes(p.T, p.K) + widened_bytes(p.N, p.K), stream);
 }
 
 cudaError_t launch_int8_input_grad(const ProductParams &p, cudaStream_t stream) {
@@ -616,7 +659,7 @@ cudaError_t launch_int8_input_grad(const ProductParams &p, cudaStream_t stream) 
     cudaError_t e = widen(p.w_codes, p.w_scale, p.N, p.K, ws, w, stream);
     if (e == cudaSuccess) e = readable_dy(p, ws + widened_bytes(p.N, p.K), dy, stream);
     if (e != cudaSuccess) return e;
-    return launch_product<false, true>(dy, w, outputs(p, p.T, p.K, p.N),
+    return launch_product<false, true, false>(dy, w, outputs(p, p.T, p.K, p.N),
                                        ws + widened_bytes(p.N, p.K) + widened_bytes(p.T, p.N), stream);
 }
 
@@ -631,7 +674,7 @@ cudaError_t launch_int8_weight_grad(const ProductParams &p, cudaStream_t stream)
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     e = widen(p.x_codes, p.x_scale, p.T, p.K, ws, x, stream);
     if (e == cudaSuccess) e = readable_dy(p, ws + widened_bytes(p.T, p.K), dy, stream);
-    if (e == cudaSuccess) e = launch_product<true, true>(dy, x, outputs(p, p.N, p.K, p.T),
+    if (e == cudaSuccess) e = launch_product<true, true, true>(dy, x, outputs(p, p.N, p.K, p.T),
                                        ws + widened_bytes(p.T, p.K) + widened_bytes(p.T, p.N), stream);
     if (e != cudaSuccess || !p.dbias) return e;
     return launch_column_sums(p, stream);
