@@ -456,7 +456,7 @@ constexpr uint32_t kMaxSplits = 16;
 // ceil(units / pairs) units, each of its steps at 512 cycles (the tensor core's rate
 // for 256 x 256 x 64) or, for the narrower tile, hardly less (its loads bound it),
 // plus a start and a store of about 3000; a split one
-// also writes and reads its sums (about 2500 bytes a cycle) in a second launch.
+// also writes and reads its sums (about 5000 bytes a cycle) in a second launch.
 // `pairs` is fixed, so that the workspace's size does not depend on the device.
 Plan plan_for(uint64_t M, uint64_t N, uint64_t L) {
     constexpr uint64_t kPairs = 76;
@@ -469,7 +469,7 @@ Plan plan_for(uint64_t M, uint64_t N, uint64_t L) {
             const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
             const uint64_t waves = (tiles * splits + kPairs - 1) / kPairs;
             double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bn == 256 ? 512 : 480) + 3000);
-            if (splits > 1) cost += 6000 + static_cast<double>(splits) * M * N * 8 / 2500;
+            if (splits > 1) cost += 6000 + static_cast<double>(splits) * M * N * 8 / 5000;
             if (cost < best_cost) {
                 best_cost = cost;
                 best = {bn, static_cast<uint32_t>(splits), static_cast<uint32_t>(per)};
