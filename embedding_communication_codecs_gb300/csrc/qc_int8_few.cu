@@ -85,8 +85,8 @@ __device__ __forceinline__ uint32_t word_of(const uint4 &v, int j) {
 }
 
 // AHEAD chunks of a warp are loaded before the first of them is multiplied.
-template <int NT, int MT, int AHEAD, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kFewWarps) few_tokens(const FewParams P) {
+template <int NT, int MT, int AHEAD, int BLOCKS, bool ALIGNED>
+__global__ void __launch_bounds__(32 * kFewWarps, BLOCKS) few_tokens(const FewParams P) {
     extern __shared__ float sums[];  // [warp][token][output], outputs padded by one
     constexpr int kOut = 16 * MT, kTok = 8 * NT, kPitch = kOut + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
@@ -150,9 +150,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_tokens(const FewParams P) 
     }
 }
 
-template <int NT, int MT, int AHEAD, bool ALIGNED>
+template <int NT, int MT, int AHEAD, int BLOCKS, bool ALIGNED>
 cudaError_t launch(const FewParams &p, cudaStream_t stream) {
-    const auto kernel = few_tokens<NT, MT, AHEAD, ALIGNED>;
+    const auto kernel = few_tokens<NT, MT, AHEAD, BLOCKS, ALIGNED>;
     constexpr size_t smem = sizeof(float) * kFewWarps * 8 * NT * (16 * MT + 1);
     if (smem > 48 * 1024) {
         const cudaError_t e = prepare_dynamic_smem(reinterpret_cast<const void *>(kernel), smem);
@@ -164,12 +164,17 @@ cudaError_t launch(const FewParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// Up to 8 tokens: where every block is resident at once with two to an SM, each
+// loads its whole share ahead (4096 x 4096: 5.5 us, against 6.2 for four blocks with
+// half of it ahead); with more blocks, more of them to an SM hide each other's ends
+// (16384 x 4096: 14.3 us against 16.1).
 template <bool ALIGNED>
 cudaError_t launch_for(const FewParams &p, cudaStream_t stream) {
-    if (p.T <= 8) return launch<1, 1, 8, ALIGNED>(p, stream);
-    if (p.T <= 16) return launch<2, 1, 4, ALIGNED>(p, stream);
-    if (p.T <= 32) return launch<4, 2, 2, ALIGNED>(p, stream);
-    return launch<8, 2, 1, ALIGNED>(p, stream);
+    if (p.T <= 8)
+        return p.N <= 16 * 304 ? launch<1, 1, 8, 2, ALIGNED>(p, stream) : launch<1, 1, 4, 4, ALIGNED>(p, stream);
+    if (p.T <= 16) return launch<2, 1, 4, 3, ALIGNED>(p, stream);
+    if (p.T <= 32) return launch<4, 2, 2, 2, ALIGNED>(p, stream);
+    return launch<8, 2, 1, 2, ALIGNED>(p, stream);
 }
 
 }  // namespace

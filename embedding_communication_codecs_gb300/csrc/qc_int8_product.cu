@@ -19,11 +19,13 @@
 // parts of a sum and store.  Every wait is bounded (qc_pipeline.cuh).
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "qc_int8_rows.cuh"
 #include "qc_internal.h"
 #include "qc_tc.cuh"
+#include "qc_tc_host.h"
 
 namespace qc {
 
@@ -87,12 +89,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
-}
-
-// One result from its whole sum.
-__device__ __forceinline__ float finish(const GemmParams &P, uint64_t m, uint64_t n, float v) {
-    if (P.m_scale) v = __fmul_rn(v, __fmul_rn(__ldg(P.m_scale + m), __ldg(P.n_scale + n)));
-    return P.bias ? __fadd_rn(v, __ldg(P.bias + n)) : v;
 }
 
 // Adds a storing warp's C columns of tensor memory to its registers.
@@ -366,14 +362,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (warp == 1) tmem_free_pair<T::kTmemCols>(tmem);
 }
 
-// The ranges of a split contraction, added in order: four columns of a row per thread.
-__global__ void __launch_bounds__(256) join(const GemmParams P) {
-    const uint64_t per_row = (P.N + 3) / 4, total = P.M * per_row, rows = (P.M + 31) / 32 * 32;
+// Four columns of a row per thread.
+__global__ void __launch_bounds__(256) join(const JoinParams P) {
+    const uint64_t per_row = (P.N + 3) / 4, total = P.M * per_row, rows = (P.M + 31) / 32 * 32, pitch = (P.N + 31) / 32 * 32;
     for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<uint64_t>(gridDim.x) * 256) {
         const uint64_t m = i / per_row, n = i % per_row * 4;
         float v[4] = {};
         for (uint32_t s = 0; s < P.splits; ++s) {
-            const float4 w = *reinterpret_cast<const float4 *>(P.partial + (s * rows + m) * P.partial_pitch + n);
+            const float4 w = *reinterpret_cast<const float4 *>(P.partial + (s * rows + m) * pitch + n);
             v[0] = __fadd_rn(v[0], w.x);
             v[1] = __fadd_rn(v[1], w.y);
             v[2] = __fadd_rn(v[2], w.z);
@@ -382,7 +378,9 @@ __global__ void __launch_bounds__(256) join(const GemmParams P) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             if (n + j >= P.N) break;
-            const float r = finish(P, m, n + j, v[j]);
+            float r = v[j];
+            if (P.m_scale) r = __fmul_rn(r, __fmul_rn(__ldg(P.m_scale + m), __ldg(P.n_scale + n + j)));
+            if (P.bias) r = __fadd_rn(r, __ldg(P.bias + n + j));
             if (P.out_bf16) {
                 static_cast<uint16_t *>(P.out)[m * P.out_stride + n + j] = to_bf16(r);
             } else {
@@ -394,22 +392,6 @@ __global__ void __launch_bounds__(256) join(const GemmParams P) {
 }
 
 // ------------------------------------------------------------------ the host
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
 
 // `rows` rows of `dim` elements `stride` apart, as boxes of box_rows rows of 128
 // bytes under the 128-byte swizzle; reads outside give zeros, writes are dropped.
@@ -434,16 +416,6 @@ bool tma_fits(const void *p, uint64_t stride, size_t esize) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride * esize % 16 == 0;
 }
 
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 2) return 1;
-    known[dev].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 // How a product of M x N results over L terms is cut.
 struct Plan {
     int bn;
@@ -460,7 +432,7 @@ constexpr uint32_t kMaxSplits = 16;
 // `pairs` is fixed, so that the workspace's size does not depend on the device.
 Plan plan_for(uint64_t M, uint64_t N, uint64_t L) {
     constexpr uint64_t kPairs = 76;
-    const uint64_t steps = (L + kStep - 1) / kStep;
+    const uint64_t steps = std::max<uint64_t>(1, (L + kStep - 1) / kStep);
     Plan best{256, 1, static_cast<uint32_t>(steps)};
     double best_cost = 1e300;
     for (int bn : {256, 128}) {
@@ -480,7 +452,6 @@ Plan plan_for(uint64_t M, uint64_t N, uint64_t L) {
 }
 
 // Sums of a split contraction: rows and row pitch in whole 32s.
-uint64_t ceil32(uint64_t v) { return (v + 31) / 32 * 32; }
 uint64_t partial_bytes(uint64_t M, uint64_t N, uint64_t L) {
     const Plan p = plan_for(M, N, L);
     return p.splits > 1 ? p.splits * ceil32(M) * ceil32(N) * 4 : 0;
@@ -521,10 +492,8 @@ cudaError_t launch_product(const Operand &a, const Operand &b, GemmParams g, voi
     if (g.splits > 1) {
         const cudaError_t e = launch_tile<A_MN, B_MN, kSums>(plan.bn, a, b, g, stream);
         if (e != cudaSuccess) return e;
-        const uint64_t work = g.M * ((g.N + 3) / 4);
-        const int grid = persistent_grid(reinterpret_cast<const void *>(&join), 256, (work + 255) / 256);
-        join<<<grid, 256, 0, stream>>>(g);
-        return cudaGetLastError();
+        return launch_join({g.partial, g.splits, g.M, g.N, g.out, g.out_stride, g.out_bf16, g.accumulate, g.m_scale,
+                            g.n_scale, g.bias}, stream);
     }
     if (!tma_fits(g.out, g.out_stride, g.out_bf16 ? 2 : 4)) return launch_tile<A_MN, B_MN, kAnywhere>(plan.bn, a, b, g, stream);
     if (g.out_bf16) return launch_tile<A_MN, B_MN, kBf16>(plan.bn, a, b, g, stream);
@@ -625,12 +594,22 @@ GemmParams outputs(const ProductParams &p, uint64_t M, uint64_t N, uint64_t L) {
 
 }  // namespace
 
-// Up to this many tokens the weights are read as codes by qc_int8_few.cu.
-constexpr uint64_t kFewTokens = 128;
+cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
+    const uint64_t work = p.M * ((p.N + 3) / 4);
+    const int grid = persistent_grid(reinterpret_cast<const void *>(&join), 256, (work + 255) / 256);
+    join<<<grid, 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+// Which kernel multiplies T tokens: the weights are read as codes by qc_int8_few.cu
+// up to kFewTokens and by qc_int8_wide.cu up to kWideTokens; beyond, the weights are
+// widened once and the tiles of this file take both operands from memory.
+constexpr uint64_t kFewTokens = 16, kWideTokens = 512;
 
 size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K) {
     if (T <= kFewTokens) return 0;
-    return widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K);
+    const size_t wide = T <= kWideTokens ? wide_tokens_workspace(T, N, K) : 0;
+    return std::max(wide, widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K));
 }
 size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
     return widened_bytes(N, K) + widened_bytes(T, N) + partial_bytes(T, K, N);
@@ -641,6 +620,7 @@ size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
     if (p.T <= kFewTokens) return launch_int8_few(p, stream);
+    if (p.T <= kWideTokens && wide_tokens_fit(p.w_codes, p.K)) return launch_int8_wide(p, stream);
     Operand x, w;
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     cudaError_t e = widen(p.x_codes, nullptr, p.T, p.K, ws, x, stream);

@@ -346,6 +346,26 @@ struct ProductParams {
     void *workspace;
 };
 
+// Sums of a contraction cut into `splits` ranges: splits x ceil32(M) rows of
+// ceil32(N) floats, added in order, scaled, biased and written as out's type.
+struct JoinParams {
+    const float *partial;
+    uint32_t splits;
+    uint64_t M, N;
+    void *out;
+    uint64_t out_stride;
+    int out_bf16, accumulate;
+    const float *m_scale, *n_scale, *bias;
+};
+inline uint64_t ceil32(uint64_t v) { return (v + 31) / 32 * 32; }
+cudaError_t launch_join(const JoinParams &p, cudaStream_t stream);
+
+// The product for a batch of tokens, the weights read as codes (qc_int8_wide.cu);
+// wide_tokens_fit(): TMA can read the weights' rows.
+bool wide_tokens_fit(const void *w_codes, uint64_t K);
+size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K);
+cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream);
+
 size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K);
 size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K);
 size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K);
@@ -380,6 +400,7 @@ cudaError_t take_encode_bf16_errors(uint32_t *flags);
 cudaError_t take_encode_bf16_fast_errors(uint32_t *flags);
 cudaError_t take_decode_errors(uint32_t *flags);
 cudaError_t take_product_errors(uint32_t *flags);
+cudaError_t take_wide_errors(uint32_t *flags);
 cudaError_t take_reencode_errors(uint32_t *flags);
 
 }  // namespace qc
