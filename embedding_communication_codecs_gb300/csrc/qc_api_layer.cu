@@ -143,7 +143,7 @@ qc_status qc_rowwise_int8_dequant(const int8_t *codes, const float *row_scale, s
     qc::RowCodesParams p{};
     p.codes_in = codes;
     p.scale_in = row_scale;
-    p.rows = rows;
+    p.rows = p.first_rows = rows;
     p.dim = static_cast<uint32_t>(dim);
     p.out = out;
     p.out_stride = out_stride;

@@ -502,18 +502,19 @@ cudaError_t launch_product(const Operand &a, const Operand &b, GemmParams g, voi
     return launch_tile<A_MN, B_MN, kF32>(plan.bn, a, b, g, stream);
 }
 
-// Column sums of bf16 rows: a block owns 32 Q columns, lane l columns Q l .. Q l + Q - 1,
-// and its 32 warps every 32nd row; the warps' fp32 sums are added in order.
+// Column sums of bf16 rows: a cluster of eight blocks owns 32 Q columns, lane l columns
+// Q l .. Q l + Q - 1, and the cluster's 64 warps every 64th row; the warps' fp32 sums
+// are added in order in each block, the blocks' in order by the first.
 template <int Q>
-__global__ void __launch_bounds__(1024) column_sums(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t cols,
-                                                    float *out, int accumulate) {
-    __shared__ float sums[32][32 * Q + 1];
-    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint64_t c = (static_cast<uint64_t>(blockIdx.x) * 32 + lane) * Q;
+__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(256)
+    column_sums(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t cols, float *out, int accumulate) {
+    __shared__ float sums[8][32 * Q + 1], total[32 * Q];
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
+    const uint64_t c = (static_cast<uint64_t>(blockIdx.x / 8) * 32 + lane) * Q;
     float s[Q] = {};
     if (c < cols) {
 #pragma unroll 8
-        for (uint64_t r = warp; r < rows; r += 32) {
+        for (uint64_t r = rank * 8 + warp; r < rows; r += 64) {
             if constexpr (Q == 2) {
                 const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(x + r * stride + c));
                 s[0] = __fadd_rn(s[0], __uint_as_float(v << 16));
@@ -526,21 +527,33 @@ __global__ void __launch_bounds__(1024) column_sums(const uint16_t *x, uint64_t 
 #pragma unroll
     for (int j = 0; j < Q; ++j) sums[warp][lane * Q + j] = s[j];
     __syncthreads();
-    const uint64_t mine = static_cast<uint64_t>(blockIdx.x) * 32 * Q + threadIdx.x;
-    if (threadIdx.x < 32 * Q && mine < cols) {
+    if (threadIdx.x < 32 * Q) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 32; ++w) v = __fadd_rn(v, sums[w][threadIdx.x]);
+        for (int w = 0; w < 8; ++w) v = __fadd_rn(v, sums[w][threadIdx.x]);
+        total[threadIdx.x] = v;
+    }
+    cluster_sync();
+    const uint64_t mine = static_cast<uint64_t>(blockIdx.x / 8) * 32 * Q + threadIdx.x;
+    if (rank == 0 && threadIdx.x < 32 * Q && mine < cols) {
+        float v = 0.0f;
+#pragma unroll
+        for (uint32_t b = 0; b < 8; ++b) {
+            float part;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part) : "r"(in_block(&total[threadIdx.x], b)) : "memory");
+            v = __fadd_rn(v, part);
+        }
         out[mine] = accumulate ? __fadd_rn(out[mine], v) : v;
     }
+    cluster_sync();  // the first block reads the others' shared memory
 }
 
 cudaError_t launch_column_sums(const ProductParams &p, cudaStream_t stream) {
     const bool pairs = p.N % 2 == 0 && p.dy_stride % 2 == 0 && (reinterpret_cast<uintptr_t>(p.dy) & 3) == 0;
     const int cols = pairs ? 64 : 32;
     const auto kernel = pairs ? column_sums<2> : column_sums<1>;
-    kernel<<<static_cast<unsigned>((p.N + cols - 1) / cols), 1024, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N, p.dbias,
-                                                                                p.accumulate);
+    kernel<<<static_cast<unsigned>(8 * ((p.N + cols - 1) / cols)), 256, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N, p.dbias,
+                                                                                    p.accumulate);
     return cudaGetLastError();
 }
 
@@ -555,17 +568,28 @@ __global__ void copy_rows(const uint16_t *x, uint64_t stride, uint64_t rows, uin
 uint64_t padded(uint64_t dim) { return (dim + 63) / 64 * 64; }
 uint64_t widened_bytes(uint64_t rows, uint64_t dim) { return (rows * padded(dim) * 2 + 255) / 256 * 256; }
 
-// Codes (times their scale, if there is one) as bf16 rows in the workspace.
-cudaError_t widen(const int8_t *codes, const float *scale, uint64_t rows, uint64_t dim, void *to, Operand &op,
-                  cudaStream_t stream) {
+// Codes (times their scale, if there is one) as bf16 rows in the workspace; two
+// matrices of one row length in one launch.
+struct Widen {
+    const int8_t *codes;
+    const float *scale;
+    uint64_t rows;
+    void *to;
+    Operand op(uint64_t dim) const { return {to, rows, dim, padded(dim)}; }
+};
+
+cudaError_t widen(uint64_t dim, const Widen &a, const Widen &b, cudaStream_t stream) {
     RowCodesParams p{};
-    p.codes_in = codes;
-    p.scale_in = scale;
-    p.rows = rows;
+    p.codes_in = a.codes;
+    p.scale_in = a.scale;
+    p.out = a.to;
+    p.first_rows = a.rows;
+    p.codes_in2 = b.codes;
+    p.scale_in2 = b.scale;
+    p.out2 = b.to;
+    p.rows = a.rows + b.rows;
     p.dim = static_cast<uint32_t>(dim);
-    p.out = to;
     p.out_stride = padded(dim);
-    op = {to, rows, dim, padded(dim)};
     return launch_rows_int8_decode(p, 1, stream);
 }
 
@@ -620,26 +644,26 @@ size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
     if (p.T <= kFewTokens) return launch_int8_few(p, stream);
-    if (p.T <= kWideTokens && wide_tokens_fit(p.w_codes, p.K)) return launch_int8_wide(p, stream);
-    Operand x, w;
+    if (p.T <= kWideTokens && wide_tokens_fit(p.x_codes, p.w_codes, p.K)) return launch_int8_wide(p, stream);
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
-    cudaError_t e = widen(p.x_codes, nullptr, p.T, p.K, ws, x, stream);
-    if (e == cudaSuccess) e = widen(p.w_codes, nullptr, p.N, p.K, ws + widened_bytes(p.T, p.K), w, stream);
+    const Widen x{p.x_codes, nullptr, p.T, ws}, w{p.w_codes, nullptr, p.N, ws + widened_bytes(p.T, p.K)};
+    const cudaError_t e = widen(p.K, x, w, stream);
     if (e != cudaSuccess) return e;
     GemmParams g = outputs(p, p.T, p.N, p.K);
     g.m_scale = p.x_scale;
     g.n_scale = p.w_scale;
     g.bias = p.bias;
-    return launch_product<false, false, false>(x, w, g, ws + widened_bytes(p.T, p.K) + widened_bytes(p.N, p.K), stream);
+    return launch_product<false, false, false>(x.op(p.K), w.op(p.K), g, ws + widened_bytes(p.T, p.K) + widened_bytes(p.N, p.K), stream);
 }
 
 cudaError_t launch_int8_input_grad(const ProductParams &p, cudaStream_t stream) {
-    Operand dy, w;
+    Operand dy;
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
-    cudaError_t e = widen(p.w_codes, p.w_scale, p.N, p.K, ws, w, stream);
+    const Widen w{p.w_codes, p.w_scale, p.N, ws};
+    cudaError_t e = widen(p.K, w, {}, stream);
     if (e == cudaSuccess) e = readable_dy(p, ws + widened_bytes(p.N, p.K), dy, stream);
     if (e != cudaSuccess) return e;
-    return launch_product<false, true, false>(dy, w, outputs(p, p.T, p.K, p.N),
+    return launch_product<false, true, false>(dy, w.op(p.K), outputs(p, p.T, p.K, p.N),
                                        ws + widened_bytes(p.N, p.K) + widened_bytes(p.T, p.N), stream);
 }
 
@@ -650,11 +674,12 @@ cudaError_t launch_int8_weight_grad(const ProductParams &p, cudaStream_t stream)
         if (e == cudaSuccess && p.dbias) e = cudaMemsetAsync(p.dbias, 0, p.N * 4, stream);
         return e;
     }
-    Operand dy, x;
+    Operand dy;
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
-    e = widen(p.x_codes, p.x_scale, p.T, p.K, ws, x, stream);
+    const Widen x{p.x_codes, p.x_scale, p.T, ws};
+    e = widen(p.K, x, {}, stream);
     if (e == cudaSuccess) e = readable_dy(p, ws + widened_bytes(p.T, p.K), dy, stream);
-    if (e == cudaSuccess) e = launch_product<true, true, true>(dy, x, outputs(p, p.N, p.K, p.T),
+    if (e == cudaSuccess) e = launch_product<true, true, true>(dy, x.op(p.K), outputs(p, p.N, p.K, p.T),
                                        ws + widened_bytes(p.T, p.K) + widened_bytes(p.T, p.N), stream);
     if (e != cudaSuccess || !p.dbias) return e;
     return launch_column_sums(p, stream);

@@ -226,10 +226,13 @@ template <typename T, int U, int V>
 __global__ void __launch_bounds__(kRowThreads) rows_decode(const RowCodesParams P, uint32_t lanes) {
     const Team team(lanes);
     const uint32_t units = P.dim / U;
-    for (uint64_t r = team.first; r < P.rows; r += team.stride) {
-        const float s = P.scale_in ? __ldg(P.scale_in + r) : 1.0f;
-        const int8_t *codes = P.codes_in + r * P.dim;
-        T *out = static_cast<T *>(P.out) + r * P.out_stride;
+    for (uint64_t row = team.first; row < P.rows; row += team.stride) {
+        const bool second = row >= P.first_rows;
+        const uint64_t r = second ? row - P.first_rows : row;
+        const float *scale = second ? P.scale_in2 : P.scale_in;
+        const float s = scale ? __ldg(scale + r) : 1.0f;
+        const int8_t *codes = (second ? P.codes_in2 : P.codes_in) + r * P.dim;
+        T *out = static_cast<T *>(second ? P.out2 : P.out) + r * P.out_stride;
         for (uint32_t base = team.lane; base < units; base += lanes * V) {
             RawCodes<U> c[V];
 #pragma unroll
@@ -426,7 +429,8 @@ template <typename T>
 cudaError_t decode_rows(const RowCodesParams &p, cudaStream_t stream) {
     constexpr int U = 16 / sizeof(T);
     const uint32_t d = p.dim;
-    if (fits(p.out, p.out_stride, sizeof(T), d, U, 16) && fits(p.codes_in, d, 1, d, U, U))
+    if (fits(p.out, p.out_stride, sizeof(T), d, U, 16) && fits(p.codes_in, d, 1, d, U, U) &&
+        (p.rows == p.first_rows || (fits(p.out2, p.out_stride, sizeof(T), d, U, 16) && fits(p.codes_in2, d, 1, d, U, U))))
         return launch_rows(rows_decode<T, U, 8>, p, lanes_for(d / U, 8, kRowThreads), kRowThreads, stream);
     return launch_rows(rows_decode<T, 1, 8>, p, lanes_for(d, 8, kRowThreads), kRowThreads, stream);
 }

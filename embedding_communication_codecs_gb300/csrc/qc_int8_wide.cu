@@ -1,22 +1,23 @@
-// qc_int8_wide.cu -- the product of the 8-bit layer for a batch of tokens, the weights
-// read from memory once and as codes.
+// qc_int8_wide.cu -- the product of the 8-bit layer for tens to hundreds of tokens, the
+// weights read from memory once and as codes.
 //
-// For tens to hundreds of tokens the weights' N K bytes are what has to be read, and
-// widening them in memory first would move five times that.  The product is turned
-// round, y^T = W X^T: the weights are the tensor core's A operand, which may come
-// from tensor memory, so a widened weight never passes through shared memory again:
+// The weights' N K bytes are what has to be read, and widening them in memory first
+// would move five times that.  The product is turned round, y^T = W X^T: the weights
+// are the tensor core's A operand, which may come from tensor memory, so a widened
+// weight never passes through shared memory again:
 //
 //     TMA -> codes in shared memory -> registers -> f16 in tensor memory -> tcgen05.mma
 //
-// (f16 holds every int8 exactly.)  The tokens are B, widened to f16 once by a small
-// launch (T K elements) and loaded by TMA.  A pair of blocks owns 256 weight rows x BT
-// tokens and a range of the contraction; per step of 128 codes each block loads 16 KB
-// of codes and half of the tokens' 256 BT bytes.  Warp 0 loads, warp 1 of the leading
-// block issues the matrix instructions, warps 4 to 11 widen (two groups of four warps
-// take alternate steps; a warp reaches 32 lanes of tensor memory), warps 12 to 15
-// store.  Tensor memory: two sums of BT columns, and four stages of 64 columns of
-// widened codes.  The lanes of a storing warp hold neighbouring outputs of one
-// token, so its stores are whole lines wherever y's rows start.
+// (f16 holds every int8 exactly.)  The tokens, B, go from codes to f16 in shared
+// memory on the way.  A block owns 128 weight rows x BT tokens and a range of the
+// contraction, in steps of 128 codes.  Warp 0 loads codes, warp 1 issues the matrix
+// instructions, and warps 4 to 15 widen and, at the end, store: three groups of four
+// (a warp reaches 32 lanes of tensor memory) take every third step, so that the
+// latency of a step, several hundred cycles of waits and conversions, is paid three
+// at a time.  The ring of kRing widened steps is as long as tensor memory (64 columns a step
+// next to BT columns of sums) and shared memory allow.
+// The lanes of a storing warp hold neighbouring outputs of one token, so its stores
+// are whole lines wherever y's rows start.
 #include <cuda.h>
 
 #include "qc_int8_rows.cuh"
@@ -32,18 +33,20 @@ QC_DEFINE_TAKE_FLAG(take_wide_errors, g_wide_error)
 namespace {
 
 constexpr int kStepK = 128;
-constexpr int kRows = 128, kPairRows = 256;
-constexpr int kThreads = 512;
-constexpr int kAStages = 4, kACols = kStepK / 2;
-constexpr int kTmemCols = 512, kATmem = 256;  // sums from column 0, widened codes from column 256
+constexpr int kRows = 128;
+constexpr int kThreads = 512, kGroups = 3;
+constexpr int kACols = kStepK / 2, kTmemCols = 512;  // sums from column 0, the ring at the end
 
 template <int BT>
 struct Wide {
-    static constexpr int kBytesW = kRows * kStepK;
-    static constexpr int kBytesX = BT / 2 * kStepK * 2;  // two boxes of BT / 2 rows of 128 bytes
-    static constexpr int kStage = kBytesW + kBytesX;
-    static constexpr int kStages = BT == 128 ? 6 : BT == 64 ? 8 : 9;
-    static constexpr int kSmem = kStages * kStage + 1024;
+    static constexpr int kBytesW = kRows * kStepK, kBytesX = BT * kStepK;  // codes of a step
+    static constexpr int kCodes = kBytesW + kBytesX;
+    static constexpr int kBytesF = BT * kStepK * 2;                       // widened tokens of a step
+    static constexpr int kRing = BT == 128 ? 3 : 7;
+    static constexpr int kStages = BT == 32 ? 8 : BT == 64 ? 4 : 3;
+    static constexpr int kFirstA = kTmemCols - kRing * kACols;
+    static constexpr int kSmem = kStages * kCodes + kRing * kBytesF + 1024;
+    static_assert(kFirstA >= BT, "the sums and the ring share tensor memory");
 };
 
 struct WideParams {
@@ -65,7 +68,7 @@ struct WideUnit {
 template <int BT>
 __device__ __forceinline__ WideUnit wide_unit(uint32_t u, const WideParams &P) {
     const uint32_t tiles_t = static_cast<uint32_t>((P.T + BT - 1) / BT);
-    const uint32_t tiles_n = static_cast<uint32_t>((P.N + kPairRows - 1) / kPairRows);
+    const uint32_t tiles_n = static_cast<uint32_t>((P.N + kRows - 1) / kRows);
     const uint32_t all = static_cast<uint32_t>((P.K + kStepK - 1) / kStepK);
     const uint32_t split = u / (tiles_t * tiles_n), first = split * P.split_steps;
     return {u / tiles_t % tiles_n, u % tiles_t, split, first, min(P.split_steps, all - first)};
@@ -80,41 +83,36 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
 }
 
 template <int BT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     wide_tokens(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const WideParams P) {
     using C = Wide<BT>;
-    constexpr int S = C::kStages;
+    constexpr int S = C::kStages, R = C::kRing;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t full_w[S], full_x[S], empty[S], a_full[kAStages], a_empty[kAStages], sums_full[2], sums_empty[2], drained;
+    __shared__ uint64_t full[S], empty[S], ready[R], freed[R], sums_full, sums_empty;
     __shared__ uint32_t tmem_slot;
-    uint8_t *const tiles = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint8_t *const widened = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);  // tokens, R steps
+    uint8_t *const codes = widened + R * C::kBytesF;                             // S steps
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank(), npairs = gridDim.x / 2, pair = blockIdx.x / 2;
-    const uint32_t units = static_cast<uint32_t>((P.T + BT - 1) / BT) * static_cast<uint32_t>((P.N + kPairRows - 1) / kPairRows) * P.splits;
+    const uint32_t units = static_cast<uint32_t>((P.T + BT - 1) / BT) * static_cast<uint32_t>((P.N + kRows - 1) / kRows) * P.splits;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full_w[s], 1);   // this block's codes
-            mbar_init(&full_x[s], 1);   // both blocks' tokens, in the leading block
-            mbar_init(&empty[s], 5);    // the four warps that widened it, and the instructions that read the tokens
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 4);  // the warps that widen it
         }
-        for (int a = 0; a < kAStages; ++a) {
-            mbar_init(&a_full[a], 8);   // four widening warps in each block, in the leading block
-            mbar_init(&a_empty[a], 1);
+        for (int r = 0; r < R; ++r) {
+            mbar_init(&ready[r], 4);  // the same warps
+            mbar_init(&freed[r], 1);  // the matrix instructions that read it
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&sums_full[b], 1);
-            mbar_init(&sums_empty[b], 8);
-        }
-        mbar_init(&drained, 1);
+        mbar_init(&sums_full, 1);
+        mbar_init(&sums_empty, 4 * kGroups);
         fence_barrier_init();
         prefetch_map(&map_w);
         prefetch_map(&map_x);
     }
-    if (warp == 1) tmem_alloc_pair<kTmemCols>(&tmem_slot);
+    if (warp == 1) tmem_alloc<kTmemCols>(&tmem_slot);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     bool ok = true;
@@ -122,174 +120,163 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             uint32_t it = 0;
-            for (uint32_t u = pair; u < units && ok; u += npairs) {
+            for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const WideUnit w = wide_unit<BT>(u, P);
-                const int n0 = static_cast<int>(w.n * kPairRows + rank * kRows), t0 = static_cast<int>(w.t * BT + rank * (BT / 2));
                 for (uint32_t k = 0; k < w.steps; ++k, ++it) {
                     const uint32_t s = it % S;
-                    if (!mbar_wait_cluster(&empty[s], ((it / S) & 1) ^ 1)) {
+                    if (!mbar_wait(&empty[s], ((it / S) & 1) ^ 1)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *codes = tiles + s * C::kStage, *x = codes + C::kBytesW;
+                    uint8_t *to = codes + s * C::kCodes;
                     const int k0 = static_cast<int>((w.first + k) * kStepK);
-                    mbar_arrive_expect_tx(&full_w[s], C::kBytesW);
-                    tma_load(codes, &map_w, k0, n0, &full_w[s]);
-                    const uint32_t bar = in_block(&full_x[s], 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&full_x[s], 2 * C::kBytesX);
-                    tma_load_pair(x, &map_x, k0, t0, bar);
-                    tma_load_pair(x + C::kBytesX / 2, &map_x, k0 + 64, t0, bar);
+                    mbar_arrive_expect_tx(&full[s], C::kCodes);
+                    tma_load(to, &map_w, k0, static_cast<int>(w.n * kRows), &full[s]);
+                    tma_load(to + C::kBytesW, &map_x, k0, static_cast<int>(w.t * BT), &full[s]);
                 }
             }
-            // no block leaves while a copy into either one is in flight
-            for (uint32_t i = it > S ? it - S : 0; i < it; ++i) {
-                ok &= mbar_wait_cluster(&full_w[i % S], (i / S) & 1);
-                if (rank == 0) ok &= mbar_wait_cluster(&full_x[i % S], (i / S) & 1);
-            }
+            // the block stays while a copy is in flight
+            for (uint32_t i = it > S ? it - S : 0; i < it; ++i) ok &= mbar_wait(&full[i % S], (i / S) & 1);
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
-            constexpr uint32_t kInstr = f16_instruction(kPairRows, BT);
+        if (lane == 0) {
+            constexpr uint32_t kInstr = f16_instruction(kRows, BT);
             uint32_t it = 0, done = 0;
-            for (uint32_t u = pair; u < units && ok; u += npairs, ++done) {
-                const uint32_t steps = wide_unit<BT>(u, P).steps, buf = done & 1;
-                if (!mbar_wait_cluster(&sums_empty[buf], ((done >> 1) & 1) ^ 1)) {
+            for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++done) {
+                const uint32_t steps = wide_unit<BT>(u, P).steps;
+                if (!mbar_wait(&sums_empty, (done & 1) ^ 1)) {
                     ok = false;
                     break;
                 }
                 for (uint32_t k = 0; k < steps; ++k, ++it) {
-                    const uint32_t s = it % S, a = it % kAStages;
-                    if (!mbar_wait_cluster(&full_x[s], (it / S) & 1) || !mbar_wait_cluster(&a_full[a], (it / kAStages) & 1)) {
+                    const uint32_t r = it % R;
+                    if (!mbar_wait(&ready[r], (it / R) & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint8_t *x = tiles + s * C::kStage + C::kBytesW;
-                    const uint64_t b0 = smem_operand(x, 0), b1 = smem_operand(x + C::kBytesX / 2, 0);
+                    const uint8_t *x = widened + r * C::kBytesF;
+                    const uint64_t b0 = smem_operand(x, 0), b1 = smem_operand(x + C::kBytesF / 2, 0);
 #pragma unroll
                     for (int j = 0; j < kStepK / 16; ++j)
-                        mma_pair_tmem(tmem + buf * BT, tmem + kATmem + a * kACols + 8 * j, (j < 4 ? b0 : b1) + (j & 3) * 2, kInstr,
-                                      k > 0 || j > 0);
-                    mma_commit_pair(&empty[s]);
-                    mma_commit_pair(&a_empty[a]);
+                        mma_tmem(tmem, tmem + C::kFirstA + r * kACols + 8 * j, (j < 4 ? b0 : b1) + (j & 3) * 2, kInstr,
+                                 k > 0 || j > 0);
+                    mma_commit(&freed[r]);
                 }
-                mma_commit_pair(&sums_full[buf]);
+                mma_commit(&sums_full);
             }
-            mma_commit_pair(&drained);
         }
-        // neither block leaves before the leading block's last instruction and the
-        // arrivals that it sent to both blocks
-        if (lane == 0) ok &= mbar_wait_cluster(&drained, 0);
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp >= 4) {
         const uint32_t group = (warp - 4) >> 2;
         const int quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t to = tmem + kATmem + (static_cast<uint32_t>(quarter * 32) << 16);
-        uint32_t it = 0;
-        for (uint32_t u = pair; u < units && ok; u += npairs) {
-            const uint32_t steps = wide_unit<BT>(u, P).steps;
-            for (uint32_t k = 0; k < steps; ++k, ++it) {
-                if ((it & 1) != group) continue;
-                const uint32_t s = it % S, a = it % kAStages;
-                ok = mbar_wait_cluster(&full_w[s], (it / S) & 1) && mbar_wait_cluster(&a_empty[a], ((it / kAStages) & 1) ^ 1);
+        const uint32_t mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);  // the warp's lanes of tensor memory
+        uint32_t it = 0, done = 0;
+        for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++done) {
+            const WideUnit w = wide_unit<BT>(u, P);
+            const uint64_t n = static_cast<uint64_t>(w.n) * kRows + row;
+            const uint32_t t0 = w.t * BT, left = static_cast<uint32_t>(P.T) - t0;
+            const bool live = n < P.N;
+            // what the stores will need, asked for before the sums are there
+            const float ws = live ? __ldg(P.w_scale + n) : 0.0f, bias = live && P.bias ? __ldg(P.bias + n) : 0.0f;
+            float xs[BT / 32];
+#pragma unroll
+            for (int i = 0; i < BT / 32; ++i) xs[i] = 32 * i + lane < left ? __ldg(P.x_scale + t0 + 32 * i + lane) : 0.0f;
+            for (uint32_t k = 0; k < w.steps; ++k, ++it) {
+                if (it % kGroups != group) continue;
+                const uint32_t s = it % S, r = it % R;
+                ok = mbar_wait(&full[s], (it / S) & 1);
+                const uint8_t *from = codes + s * C::kCodes;
+                uint4 c[8], x[BT / 16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const uint4 *>(from + row * 128 + ((i ^ (row & 7)) << 4));
+                // 16 codes of token t, piece p of its eight
+#pragma unroll
+                for (int i = 0; i < BT / 16; ++i) {
+                    const int t = i * 16 + (row >> 3), p = row & 7;
+                    x[i] = *reinterpret_cast<const uint4 *>(from + C::kBytesW + t * 128 + ((p ^ (t & 7)) << 4));
+                }
+                ok = ok && mbar_wait(&freed[r], ((it / R) & 1) ^ 1);
                 if (__any_sync(kFull, !ok)) {
                     ok = false;
                     break;
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);  // the whole warp has read its codes
                 tc_fence_after();
-                const uint8_t *codes = tiles + s * C::kStage + row * 128;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t f[32];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint4 c = *reinterpret_cast<const uint4 *>(codes + (((4 * h + i) ^ (row & 7)) << 4));
-                        widen4(c.x, f[8 * i], f[8 * i + 1]);
-                        widen4(c.y, f[8 * i + 2], f[8 * i + 3]);
-                        widen4(c.z, f[8 * i + 4], f[8 * i + 5]);
-                        widen4(c.w, f[8 * i + 6], f[8 * i + 7]);
+                        widen4(c[4 * h + i].x, f[8 * i], f[8 * i + 1]);
+                        widen4(c[4 * h + i].y, f[8 * i + 2], f[8 * i + 3]);
+                        widen4(c[4 * h + i].z, f[8 * i + 4], f[8 * i + 5]);
+                        widen4(c[4 * h + i].w, f[8 * i + 6], f[8 * i + 7]);
                     }
-                    tmem_store32(to + a * kACols + 32 * h, f);
+                    tmem_store32(mine + C::kFirstA + r * kACols + 32 * h, f);
                 }
+                uint8_t *to = widened + r * C::kBytesF;
+#pragma unroll
+                for (int i = 0; i < BT / 16; ++i) {
+                    const int t = i * 16 + (row >> 3), p = row & 7;
+                    uint4 lo, hi;
+                    widen4(x[i].x, lo.x, lo.y);
+                    widen4(x[i].y, lo.z, lo.w);
+                    widen4(x[i].z, hi.x, hi.y);
+                    widen4(x[i].w, hi.z, hi.w);
+                    uint8_t *at = to + (p >> 2) * (C::kBytesF / 2) + t * 128;
+                    *reinterpret_cast<uint4 *>(at + (((2 * (p & 3)) ^ (t & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4 *>(at + (((2 * (p & 3) + 1) ^ (t & 7)) << 4)) = hi;
+                }
+                fence_proxy_async_shared();
                 tmem_wait_store();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&empty[s]);
-                    mbar_arrive_cluster(in_block(&a_full[a], 0));
-                }
+                if (lane == 0) mbar_arrive(&ready[r]);
             }
-        }
-    } else if (warp >= 12) {
-        const int quarter = warp & 3;
-        uint32_t done = 0;
-        for (uint32_t u = pair; u < units; u += npairs, ++done) {
-            const uint32_t buf = done & 1;
-            ok = mbar_wait_cluster(&sums_full[buf], (done >> 1) & 1);
+            if (ok) ok = mbar_wait(&sums_full, done & 1);
             if (__any_sync(kFull, !ok)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const WideUnit w = wide_unit<BT>(u, P);
-            const uint64_t n = static_cast<uint64_t>(w.n) * kPairRows + rank * kRows + quarter * 32 + lane;
-            const uint64_t t0 = static_cast<uint64_t>(w.t) * BT;
-            const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * BT;
-            const bool live = n < P.N;
-            const float ws = live ? __ldg(P.w_scale + n) : 0.0f, bias = live && P.bias ? __ldg(P.bias + n) : 0.0f;
             const uint64_t rows = (P.T + 31) / 32 * 32, pitch = (P.N + 31) / 32 * 32;
-#pragma unroll 1
-            for (int c = 0; c < BT && t0 + c < P.T; c += 8) {
-                uint32_t v[8];
-                tmem_load8(from + c, v);
-                tmem_wait_load();
-                if (live) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint64_t t = t0 + c + j;
-                        if (t >= P.T) break;
-                        float r = __uint_as_float(v[j]);
-                        if (P.splits > 1) {
-                            P.partial[(w.split * rows + t) * pitch + n] = r;
-                            continue;
-                        }
-                        r = __fmul_rn(r, __fmul_rn(__ldg(P.x_scale + t), ws));
-                        if (P.bias) r = __fadd_rn(r, bias);
-                        if (P.y_bf16)
-                            static_cast<uint16_t *>(P.y)[t * P.y_stride + n] = to_bf16(r);
-                        else
-                            static_cast<float *>(P.y)[t * P.y_stride + n] = r;
+            for (int c = 0; c < BT; c += 8) {
+                if (c >= left) break;
+                if ((c / 8) % kGroups != group) continue;
+                uint32_t v[8];
+                tmem_load8(mine + c, v);
+                tmem_wait_load();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float xt = __shfl_sync(kFull, xs[c / 32], (c + j) & 31);
+                    if (c + j >= left || !live) continue;
+                    const uint64_t t = t0 + c + j;
+                    float y = __uint_as_float(v[j]);
+                    if (P.splits > 1) {
+                        P.partial[(w.split * rows + t) * pitch + n] = y;
+                        continue;
                     }
+                    y = __fmul_rn(y, __fmul_rn(xt, ws));
+                    if (P.bias) y = __fadd_rn(y, bias);
+                    if (P.y_bf16)
+                        static_cast<uint16_t *>(P.y)[t * P.y_stride + n] = to_bf16(y);
+                    else
+                        static_cast<float *>(P.y)[t * P.y_stride + n] = y;
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(in_block(&sums_empty[buf], 0));
+            if (lane == 0) mbar_arrive(&sums_empty);
         }
     }
     if (!ok) report_failure(&g_wide_error, P.status, kErrPipelineTimeout);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
-    if (warp == 1) tmem_free_pair<kTmemCols>(tmem);
-}
-
-// Codes of a row -> f16, eight at a time where rows start on 8 bytes.
-template <int U>
-__global__ void __launch_bounds__(256) widen_tokens(const int8_t *codes, uint64_t T, uint64_t K, uint16_t *out, uint64_t pitch) {
-    const uint64_t per_row = K / U, total = T * per_row;
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<uint64_t>(gridDim.x) * 256) {
-        const uint64_t t = i / per_row, k = i % per_row * U;
-        if constexpr (U == 8) {
-            const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + t * K + k));
-            uint4 f;
-            widen4(c.x, f.x, f.y);
-            widen4(c.y, f.z, f.w);
-            *reinterpret_cast<uint4 *>(out + t * pitch + k) = f;
-        } else {
-            uint32_t lo, hi;
-            widen4(static_cast<uint8_t>(codes[t * K + k]), lo, hi);
-            out[t * pitch + k] = static_cast<uint16_t>(lo & 0xFFFFu);
-        }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_free<kTmemCols>(tmem);
     }
 }
 
@@ -298,22 +285,22 @@ struct WidePlan {
     uint32_t splits, split_steps;
 };
 
-// Token tiles of 32, 64 or 128, and the contraction cut so that about 76 pairs have
-// work: a step takes a pair about 700 cycles at its share of the memory's rate, or
-// the tensor core's 4 BT; a unit starts and stores in about 3000; a join is a launch
-// and its sums written and read.
+// Token tiles of 32, 64 or 128, and the contraction cut so that the SMs have work: a
+// step takes a block about 700 cycles at its share of the memory's rate (1000 with the
+// short ring of 128 tokens); a unit starts and stores in about 5000; a join is a
+// launch and its sums written and read.
 WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
-    constexpr uint64_t kPairs = 76;
+    constexpr uint64_t kBlocks = 152;
     const int bt = T <= 32 ? 32 : T <= 64 ? 64 : 128;
     const uint64_t steps = (K + kStepK - 1) / kStepK;
-    const uint64_t tiles = ((T + bt - 1) / bt) * ((N + kPairRows - 1) / kPairRows);
+    const uint64_t tiles = ((T + bt - 1) / bt) * ((N + kRows - 1) / kRows);
     WidePlan best{bt, 1, static_cast<uint32_t>(steps)};
     double best_cost = 1e300;
     for (uint64_t s = 1; s <= 16 && (s == 1 || steps / s >= 2); ++s) {
         const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
-        const uint64_t waves = (tiles * splits + kPairs - 1) / kPairs;
-        double cost = static_cast<double>(waves) * (static_cast<double>(per) * 700 + 3000);
-        if (splits > 1) cost += 5000 + static_cast<double>(splits) * T * N * 8 / 5000;
+        const uint64_t waves = (tiles * splits + kBlocks - 1) / kBlocks;
+        double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bt == 128 ? 1000 : 700) + 5000);
+        if (splits > 1) cost += 6000 + static_cast<double>(splits) * T * N * 8 / 5000;
         if (cost < best_cost) {
             best_cost = cost;
             best = {bt, static_cast<uint32_t>(splits), static_cast<uint32_t>(per)};
@@ -322,62 +309,49 @@ WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     return best;
 }
 
-uint64_t pitch_of(uint64_t K) { return (K + 63) / 64 * 64; }
-uint64_t tokens_bytes(uint64_t T, uint64_t K) { return (T * pitch_of(K) * 2 + 255) / 256 * 256; }
-
-bool map_rows(CUtensorMap *map, CUtensorMapDataType type, const void *p, uint64_t rows, uint64_t dim, uint64_t stride_bytes,
-              uint32_t box_dim, uint32_t box_rows) {
-    const cuuint64_t dims[2] = {dim, rows}, strides[1] = {stride_bytes};
-    const cuuint32_t box[2] = {box_dim, box_rows}, unit[2] = {1, 1};
+// Rows of K codes as boxes of 128 codes under the 128-byte swizzle; zeros outside.
+bool map_codes(CUtensorMap *map, const int8_t *p, uint64_t rows, uint64_t K, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {K, rows}, strides[1] = {K};
+    const cuuint32_t box[2] = {kStepK, box_rows}, unit[2] = {1, 1};
     EncodeTiled fn = encode_tiled();
-    return fn && fn(map, type, 2, const_cast<void *>(p), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(p), dims, strides, box, unit,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int BT>
-cudaError_t launch_wide(const ProductParams &p, const uint16_t *x, const WideParams &w, cudaStream_t stream) {
+cudaError_t launch_wide(const ProductParams &p, const WideParams &w, cudaStream_t stream) {
     using C = Wide<BT>;
     const auto kernel = wide_tokens<BT>;
     CUtensorMap mw, mx;
-    if (!map_rows(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.w_codes, p.N, p.K, p.K, kStepK, kRows) ||
-        !map_rows(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, p.T, p.K, pitch_of(p.K) * 2, 64, BT / 2))
-        return cudaErrorInvalidValue;
+    if (!map_codes(&mw, p.w_codes, p.N, p.K, kRows) || !map_codes(&mx, p.x_codes, p.T, p.K, BT)) return cudaErrorInvalidValue;
     const cudaError_t e = prepare_dynamic_smem(reinterpret_cast<const void *>(kernel), C::kSmem);
     if (e != cudaSuccess) return e;
-    const uint64_t units = ((p.T + BT - 1) / BT) * ((p.N + kPairRows - 1) / kPairRows) * w.splits;
-    const uint64_t most = sm_count() / 2;
-    kernel<<<static_cast<unsigned>(2 * (units < most ? units : most)), kThreads, C::kSmem, stream>>>(mw, mx, w);
+    const uint64_t units = ((p.T + BT - 1) / BT) * ((p.N + kRows - 1) / kRows) * w.splits, most = sm_count();
+    kernel<<<static_cast<unsigned>(units < most ? units : most), kThreads, C::kSmem, stream>>>(mw, mx, w);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-bool wide_tokens_fit(const void *w_codes, uint64_t K) {
-    return K % 16 == 0 && (reinterpret_cast<uintptr_t>(w_codes) & 15) == 0;
+bool wide_tokens_fit(const void *x_codes, const void *w_codes, uint64_t K) {
+    return K % 16 == 0 && ((reinterpret_cast<uintptr_t>(x_codes) | reinterpret_cast<uintptr_t>(w_codes)) & 15) == 0;
 }
 
 size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K) {
     const WidePlan plan = wide_plan(T, N, K);
-    return tokens_bytes(T, K) + (plan.splits > 1 ? plan.splits * ceil32(T) * ceil32(N) * 4 : 0);
+    return plan.splits > 1 ? plan.splits * ceil32(T) * ceil32(N) * 4 : 0;
 }
 
 cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream) {
     const WidePlan plan = wide_plan(p.T, p.N, p.K);
-    uint16_t *x = static_cast<uint16_t *>(p.workspace);
-    const bool eights = p.K % 8 == 0 && (reinterpret_cast<uintptr_t>(p.x_codes) & 7) == 0;
-    const auto widen = eights ? widen_tokens<8> : widen_tokens<1>;
-    const uint64_t work = p.T * (eights ? p.K / 8 : p.K);
-    widen<<<persistent_grid(reinterpret_cast<const void *>(widen), 256, (work + 255) / 256), 256, 0, stream>>>(p.x_codes, p.T, p.K, x,
-                                                                                                         pitch_of(p.K));
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
     WideParams w{};
     w.T = p.T;
     w.N = p.N;
     w.K = p.K;
     w.splits = plan.splits;
     w.split_steps = plan.split_steps;
-    w.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + tokens_bytes(p.T, p.K));
+    w.partial = static_cast<float *>(p.workspace);
     w.y = p.out;
     w.y_stride = p.out_stride;
     w.y_bf16 = p.out_bf16;
@@ -385,8 +359,9 @@ cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream) {
     w.w_scale = p.w_scale;
     w.bias = p.bias;
     w.status = p.status;
-    e = plan.bt == 32 ? launch_wide<32>(p, x, w, stream) : plan.bt == 64 ? launch_wide<64>(p, x, w, stream)
-                                                                         : launch_wide<128>(p, x, w, stream);
+    const cudaError_t e = plan.bt == 32   ? launch_wide<32>(p, w, stream)
+                          : plan.bt == 64 ? launch_wide<64>(p, w, stream)
+                                          : launch_wide<128>(p, w, stream);
     if (e != cudaSuccess || w.splits == 1) return e;
     return launch_join({w.partial, w.splits, p.T, p.N, p.out, p.out_stride, p.out_bf16, 0, p.x_scale, p.w_scale, p.bias}, stream);
 }

@@ -305,6 +305,12 @@ struct RowCodesParams {
     const float *scale_in;  // or null: the codes themselves (decode only)
     void *out;
     uint64_t out_stride;
+    // decode only: rows from first_rows on are a second matrix of the same dim and
+    // out_stride (without one, first_rows is rows)
+    uint64_t first_rows;
+    const int8_t *codes_in2;
+    const float *scale_in2;
+    void *out2;
 };
 
 struct SwigluParams {
@@ -361,8 +367,8 @@ inline uint64_t ceil32(uint64_t v) { return (v + 31) / 32 * 32; }
 cudaError_t launch_join(const JoinParams &p, cudaStream_t stream);
 
 // The product for a batch of tokens, the weights read as codes (qc_int8_wide.cu);
-// wide_tokens_fit(): TMA can read the weights' rows.
-bool wide_tokens_fit(const void *w_codes, uint64_t K);
+// wide_tokens_fit(): TMA can read the rows of both.
+bool wide_tokens_fit(const void *x_codes, const void *w_codes, uint64_t K);
 size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K);
 cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream);
 

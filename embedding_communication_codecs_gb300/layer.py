@@ -14,8 +14,6 @@ stream they run on, and return the results.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import (QC_ACCUMULATE_INTO_OUT, QC_DTYPE_BF16, QC_DTYPE_F32, _check, _need, _on_device, _ptr,
@@ -158,15 +156,21 @@ def qc_swiglu_backward(dh, dtype, dh_stride, saved_codes, saved_scale, rows, dim
 
 
 # -------------------------------------------------------------- conveniences
+#
+# Each call first asks, in one expression, whether its tensors are plainly right
+# (dense, of the expected types and shapes, on a CUDA device); only if not does it
+# look closer, to accept a strided matrix or to say what is wrong.  For a call of a
+# few microseconds on the GPU, the host's time is what counts.
 
-def _rows(t, name, dtypes, shape=None):
-    """A matrix whose rows are dense: its shape is checked, its row stride returned."""
+_empty = torch.empty
+
+
+def _rows(t, name, dtypes):
+    """A matrix whose rows are dense: its row stride."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
     if t.dtype not in dtypes:
-        raise ValueError(f"{name} has dtype {t.dtype}; expected one of {dtypes}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {shape}")
+        raise ValueError(f"{name} has dtype {t.dtype}; expected one of {tuple(dtypes)}")
     r, d = t.shape
     if d > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be dense along its last dimension")
@@ -184,13 +188,25 @@ def _dense(t, name, dtypes, shape):
 
 
 def _codes(codes, scale, what):
-    """Row codes and their scales: the shape of the matrix they stand for."""
+    """Row codes and their scales."""
     if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
         raise ValueError(f"{what}_codes must be a 2-D tensor")
     shape = tuple(codes.shape)
     _dense(codes, f"{what}_codes", _I8, shape)
     _dense(scale, f"{what}_scale", _F32, (shape[0],))
-    return shape
+
+
+def _plain_codes(codes, scale):
+    """Dense row codes and scales on a CUDA device."""
+    return (isinstance(codes, torch.Tensor) and isinstance(scale, torch.Tensor) and codes.dim() == 2
+            and codes.dtype is torch.int8 and scale.dtype is torch.float32 and scale.shape == codes.shape[:1]
+            and codes.is_contiguous() and scale.is_contiguous() and codes.is_cuda and scale.is_cuda)
+
+
+def _plain_rows(t):
+    """A dense fp32 or bf16 matrix on a CUDA device."""
+    return (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _CODE_OF and t.is_contiguous()
+            and t.is_cuda)
 
 
 def _dtype(dtype):
@@ -202,88 +218,121 @@ def _dtype(dtype):
 def _on(stream):
     """Results and workspaces belong to the stream that the call runs on, so that the
     allocator reuses their memory in that stream's order."""
-    if stream is None:
-        return contextlib.nullcontext()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)
 
 
-def _raw_stream(stream, t):
-    """The stream's handle; without one, the current stream of t's device (one lookup,
-    without the Stream object that torch.cuda.current_stream() builds)."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    return _stream(stream)
-
-
-def _scratch(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _current(t):
+    """The handle of the current stream of t's device (one lookup, without the Stream
+    object that torch.cuda.current_stream() builds)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def rowwise_int8(x, *, stream=None):
     """int8 codes of x's shape and one fp32 power-of-two scale per row.
 
     ``x`` is [rows, dim] fp32 or bf16 with dense rows."""
-    stride = _rows(x, "x", (torch.float32, torch.bfloat16))
-    _on_device(x=x)
+    if stream is not None:
+        with _on(stream):
+            return rowwise_int8(x)
+    if _plain_rows(x):
+        stride = x.shape[1]
+    else:
+        stride = _rows(x, "x", _CODE_OF)
+        _on_device(x=x)
     rows, dim = x.shape
-    with _on(stream):
-        codes = torch.empty((rows, dim), dtype=torch.int8, device=x.device)
-        scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
-        _check(lib.qc_rowwise_int8(x.data_ptr(), _CODE_OF[x.dtype], stride, rows, dim, codes.data_ptr(),
-                                   scale.data_ptr(), _raw_stream(stream, x)))
+    device = x.device
+    codes = _empty((rows, dim), dtype=torch.int8, device=device)
+    scale = _empty((rows,), dtype=torch.float32, device=device)
+    status = lib.qc_rowwise_int8(x.data_ptr(), _CODE_OF[x.dtype], stride, rows, dim, codes.data_ptr(),
+                                 scale.data_ptr(), _current(x))
+    if status:
+        _check(status)
     return codes, scale
 
 
 def rowwise_int8_dequant(codes, row_scale, *, dtype=torch.bfloat16, stream=None):
     """The rows that the codes stand for."""
-    rows, dim = _codes(codes, row_scale, "row")
+    if stream is not None:
+        with _on(stream):
+            return rowwise_int8_dequant(codes, row_scale, dtype=dtype)
     code = _dtype(dtype)
-    _on_device(codes=codes, row_scale=row_scale)
-    with _on(stream):
-        out = torch.empty((rows, dim), dtype=dtype, device=codes.device)
-        _check(lib.qc_rowwise_int8_dequant(codes.data_ptr(), row_scale.data_ptr(), rows, dim,
-                                           out.data_ptr(), code, dim, _raw_stream(stream, codes)))
+    if not _plain_codes(codes, row_scale):
+        _codes(codes, row_scale, "row")
+        _on_device(codes=codes, row_scale=row_scale)
+    rows, dim = codes.shape
+    out = _empty((rows, dim), dtype=dtype, device=codes.device)
+    status = lib.qc_rowwise_int8_dequant(codes.data_ptr(), row_scale.data_ptr(), rows, dim, out.data_ptr(),
+                                         code, dim, _current(codes))
+    if status:
+        _check(status)
     return out
 
 
 def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bfloat16, stream=None):
     """y [T, N] from the codes of x [T, K] and of w [N, K], their scales, and an
     optional fp32 bias [N]."""
-    T, K = _codes(x_codes, x_scale, "x")
-    N, kw = _codes(w_codes, w_scale, "w")
+    if stream is not None:
+        with _on(stream):
+            return int8_matmul(x_codes, x_scale, w_codes, w_scale, bias, dtype=dtype)
+    code = _dtype(dtype)
+    plain = _plain_codes(x_codes, x_scale) and _plain_codes(w_codes, w_scale)
+    if not plain:
+        _codes(x_codes, x_scale, "x")
+        _codes(w_codes, w_scale, "w")
+    if bias is not None:
+        _dense(bias, "bias", _F32, (w_codes.shape[0],))
+        plain = plain and bias.is_cuda
+    T, K = x_codes.shape
+    N, kw = w_codes.shape
     if kw != K:
         raise ValueError(f"w_codes has rows of {kw}, x_codes of {K}")
-    if bias is not None:
-        _dense(bias, "bias", _F32, (N,))
-    code = _dtype(dtype)
-    _on_device(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias)
-    with _on(stream):
-        y = torch.empty((T, N), dtype=dtype, device=x_codes.device)
-        nbytes = lib.qc_int8_matmul_workspace(T, N, K)
-        ws = _scratch(nbytes, x_codes.device)
-        _check(lib.qc_int8_matmul(x_codes.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
-                                  w_scale.data_ptr(), _ptr(bias), T, N, K, y.data_ptr(), code, N,
-                                  _ptr(ws), nbytes, _raw_stream(stream, x_codes)))
+    device = x_codes.device
+    if not plain:
+        _on_device(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias)
+    y = _empty((T, N), dtype=dtype, device=device)
+    nbytes = lib.qc_int8_matmul_workspace(T, N, K)
+    ws = _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    status = lib.qc_int8_matmul(x_codes.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
+                                w_scale.data_ptr(), None if bias is None else bias.data_ptr(), T, N, K,
+                                y.data_ptr(), code, N, ws.data_ptr() if nbytes else None, nbytes,
+                                _current(x_codes))
+    if status:
+        _check(status)
     return y
+
+
+def _plain_dy(dy):
+    return (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype is torch.bfloat16
+            and dy.is_contiguous() and dy.is_cuda)
 
 
 def int8_input_grad(dy, w_codes, w_scale, *, dtype=torch.bfloat16, stream=None):
     """dx [T, K] from dy [T, N] bf16 (dense rows) and the codes of w [N, K]."""
-    N, K = _codes(w_codes, w_scale, "w")
-    stride = _rows(dy, "dy", _BF16)
-    T = dy.shape[0]
-    if dy.shape[1] != N:
-        raise ValueError(f"dy has rows of {dy.shape[1]}, w_codes has {N} rows")
+    if stream is not None:
+        with _on(stream):
+            return int8_input_grad(dy, w_codes, w_scale, dtype=dtype)
     code = _dtype(dtype)
-    _on_device(dy=dy, w_codes=w_codes, w_scale=w_scale)
-    with _on(stream):
-        dx = torch.empty((T, K), dtype=dtype, device=dy.device)
-        nbytes = lib.qc_int8_input_grad_workspace(T, N, K)
-        ws = _scratch(nbytes, dy.device)
-        _check(lib.qc_int8_input_grad(dy.data_ptr(), stride, w_codes.data_ptr(), w_scale.data_ptr(), T, N,
-                                      K, dx.data_ptr(), code, K, _ptr(ws), nbytes, _raw_stream(stream, dy)))
+    plain = _plain_codes(w_codes, w_scale) and _plain_dy(dy)
+    if not plain:
+        _codes(w_codes, w_scale, "w")
+        _rows(dy, "dy", _BF16)
+    N, K = w_codes.shape
+    T, n = dy.shape
+    if n != N:
+        raise ValueError(f"dy has rows of {n}, w_codes has {N} rows")
+    if not plain:
+        _on_device(dy=dy, w_codes=w_codes, w_scale=w_scale)
+    device = dy.device
+    dx = _empty((T, K), dtype=dtype, device=device)
+    nbytes = lib.qc_int8_input_grad_workspace(T, N, K)
+    ws = _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    status = lib.qc_int8_input_grad(dy.data_ptr(), dy.stride(0) if T > 1 else N, w_codes.data_ptr(),
+                                    w_scale.data_ptr(), T, N, K, dx.data_ptr(), code, K,
+                                    ws.data_ptr() if nbytes else None, nbytes, _current(dy))
+    if status:
+        _check(status)
     return dx
 
 
@@ -292,64 +341,90 @@ def int8_weight_grad(dy, x_codes, x_scale, *, dtype=torch.float32, with_bias=Fal
     """(dw [N, K], dbias [N] fp32 or None) from dy [T, N] bf16 (dense rows) and the
     codes of x [T, K].  ``into`` = (dw, dbias or None), fp32: the gradients are
     added to them and they are returned."""
-    T, K = _codes(x_codes, x_scale, "x")
-    stride = _rows(dy, "dy", _BF16)
-    N = dy.shape[1]
-    if dy.shape[0] != T:
-        raise ValueError(f"dy has {dy.shape[0]} rows, x_codes {T}")
+    if stream is not None:
+        with _on(stream):
+            return int8_weight_grad(dy, x_codes, x_scale, dtype=dtype, with_bias=with_bias, into=into)
+    plain = _plain_codes(x_codes, x_scale) and _plain_dy(dy)
+    if not plain:
+        _codes(x_codes, x_scale, "x")
+        _rows(dy, "dy", _BF16)
+    T, K = x_codes.shape
+    t, N = dy.shape
+    if t != T:
+        raise ValueError(f"dy has {t} rows, x_codes {T}")
     if into is not None:
         dw, dbias = into
+        dtype = torch.float32
         _dense(dw, "dw", _F32, (N, K))
         if dbias is not None:
             _dense(dbias, "dbias", _F32, (N,))
         _on_device(dw=dw, dbias=dbias)
-        dtype = torch.float32
     code = _dtype(dtype)
-    _on_device(dy=dy, x_codes=x_codes, x_scale=x_scale)
-    with _on(stream):
-        if into is None:
-            dw = torch.empty((N, K), dtype=dtype, device=dy.device)
-            dbias = torch.empty((N,), dtype=torch.float32, device=dy.device) if with_bias else None
-        nbytes = lib.qc_int8_weight_grad_workspace(T, N, K)
-        ws = _scratch(nbytes, dy.device)
-        _check(lib.qc_int8_weight_grad(dy.data_ptr(), stride, x_codes.data_ptr(), x_scale.data_ptr(), T, N,
-                                       K, dw.data_ptr(), code, _ptr(dbias),
-                                       0 if into is None else QC_ACCUMULATE_INTO_OUT, _ptr(ws), nbytes,
-                                       _raw_stream(stream, dy)))
+    if not plain:
+        _on_device(dy=dy, x_codes=x_codes, x_scale=x_scale)
+    device = dy.device
+    if into is None:
+        dw = _empty((N, K), dtype=dtype, device=device)
+        dbias = _empty((N,), dtype=torch.float32, device=device) if with_bias else None
+    nbytes = lib.qc_int8_weight_grad_workspace(T, N, K)
+    ws = _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    status = lib.qc_int8_weight_grad(dy.data_ptr(), dy.stride(0) if T > 1 else N, x_codes.data_ptr(),
+                                     x_scale.data_ptr(), T, N, K, dw.data_ptr(), code,
+                                     None if dbias is None else dbias.data_ptr(),
+                                     0 if into is None else QC_ACCUMULATE_INTO_OUT,
+                                     ws.data_ptr() if nbytes else None, nbytes, _current(dy))
+    if status:
+        _check(status)
     return dw, dbias
 
 
 def swiglu_encode(gate_up, *, stream=None):
     """(h_codes [T, F], h_scale [T], saved_codes [T, 2F], saved_scale [T, 2]) of
     gate_up [T, 2F], a row's F gates followed by its F ups (dense rows, fp32 or bf16)."""
-    stride = _rows(gate_up, "gate_up", (torch.float32, torch.bfloat16))
+    if stream is not None:
+        with _on(stream):
+            return swiglu_encode(gate_up)
+    if _plain_rows(gate_up):
+        stride = gate_up.shape[1]
+    else:
+        stride = _rows(gate_up, "gate_up", _CODE_OF)
     rows, two = gate_up.shape
     if two % 2:
         raise ValueError(f"gate_up has rows of {two}; an even number is needed")
-    dim, dev = two // 2, gate_up.device
-    _on_device(gate_up=gate_up)
-    with _on(stream):
-        h_codes = torch.empty((rows, dim), dtype=torch.int8, device=dev)
-        h_scale = torch.empty((rows,), dtype=torch.float32, device=dev)
-        saved_codes = torch.empty((rows, two), dtype=torch.int8, device=dev)
-        saved_scale = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-        _check(lib.qc_swiglu_encode(gate_up.data_ptr(), _CODE_OF[gate_up.dtype], stride, rows, dim,
-                                    h_codes.data_ptr(), h_scale.data_ptr(), saved_codes.data_ptr(),
-                                    saved_scale.data_ptr(), _raw_stream(stream, gate_up)))
+    device = gate_up.device
+    if device.type != "cuda":
+        _on_device(gate_up=gate_up)
+    dim = two // 2
+    h_codes = _empty((rows, dim), dtype=torch.int8, device=device)
+    h_scale = _empty((rows,), dtype=torch.float32, device=device)
+    saved_codes = _empty((rows, two), dtype=torch.int8, device=device)
+    saved_scale = _empty((rows, 2), dtype=torch.float32, device=device)
+    status = lib.qc_swiglu_encode(gate_up.data_ptr(), _CODE_OF[gate_up.dtype], stride, rows, dim,
+                                  h_codes.data_ptr(), h_scale.data_ptr(), saved_codes.data_ptr(),
+                                  saved_scale.data_ptr(), _current(gate_up))
+    if status:
+        _check(status)
     return h_codes, h_scale, saved_codes, saved_scale
 
 
 def swiglu_backward(dh, saved_codes, saved_scale, *, stream=None):
     """dgate_up [T, 2F] of dh's type from dh [T, F] (dense rows, fp32 or bf16) and
     what swiglu_encode saved."""
-    stride = _rows(dh, "dh", (torch.float32, torch.bfloat16))
+    if stream is not None:
+        with _on(stream):
+            return swiglu_backward(dh, saved_codes, saved_scale)
+    if _plain_rows(dh):
+        stride = dh.shape[1]
+    else:
+        stride = _rows(dh, "dh", _CODE_OF)
     rows, dim = dh.shape
     _dense(saved_codes, "saved_codes", _I8, (rows, 2 * dim))
     _dense(saved_scale, "saved_scale", _F32, (rows, 2))
-    _on_device(dh=dh, saved_codes=saved_codes, saved_scale=saved_scale)
-    with _on(stream):
-        out = torch.empty((rows, 2 * dim), dtype=dh.dtype, device=dh.device)
-        _check(lib.qc_swiglu_backward(dh.data_ptr(), _CODE_OF[dh.dtype], stride, saved_codes.data_ptr(),
-                                      saved_scale.data_ptr(), rows, dim, out.data_ptr(), 2 * dim,
-                                      _raw_stream(stream, dh)))
+    if not (dh.is_cuda and saved_codes.is_cuda and saved_scale.is_cuda):
+        _on_device(dh=dh, saved_codes=saved_codes, saved_scale=saved_scale)
+    out = _empty((rows, 2 * dim), dtype=dh.dtype, device=dh.device)
+    status = lib.qc_swiglu_backward(dh.data_ptr(), _CODE_OF[dh.dtype], stride, saved_codes.data_ptr(),
+                                    saved_scale.data_ptr(), rows, dim, out.data_ptr(), 2 * dim, _current(dh))
+    if status:
+        _check(status)
     return out
