@@ -35,7 +35,8 @@ namespace {
 constexpr int kStepK = 128;
 constexpr int kRows = 128;
 constexpr int kThreads = 512, kGroups = 3;
-constexpr int kACols = kStepK / 2, kTmemCols = 512;  // sums from column 0, the ring at the end
+// All of tensor memory, so it starts at column 0: the sums there, the ring at the end.
+constexpr int kACols = kStepK / 2, kTmemCols = 512;
 
 template <int BT>
 struct Wide {
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t tmem_slot;
     uint8_t *const widened = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);  // tokens, R steps
     uint8_t *const codes = widened + R * C::kBytesF;                             // S steps
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t units = static_cast<uint32_t>((P.T + BT - 1) / BT) * static_cast<uint32_t>((P.N + kRows - 1) / kRows) * P.splits;
 
     if (threadIdx.x == 0) {
@@ -114,7 +115,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
     bool ok = true;
 
     if (warp == 0) {
@@ -139,37 +139,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t i = it > S ? it - S : 0; i < it; ++i) ok &= mbar_wait(&full[i % S], (i / S) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t kInstr = f16_instruction(kRows, BT);
-            uint32_t it = 0, done = 0;
-            for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++done) {
-                const uint32_t steps = wide_unit<BT>(u, P).steps;
-                if (!mbar_wait(&sums_empty, (done & 1) ^ 1)) {
-                    ok = false;
-                    break;
-                }
-                for (uint32_t k = 0; k < steps; ++k, ++it) {
-                    const uint32_t r = it % R;
-                    if (!mbar_wait(&ready[r], (it / R) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint8_t *x = widened + r * C::kBytesF;
-                    const uint64_t b0 = smem_operand(x, 0), b1 = smem_operand(x + C::kBytesF / 2, 0);
+        // the whole warp goes round, one lane issues
+        constexpr uint32_t kInstr = f16_instruction(kRows, BT);
+        const bool issues = one_lane();
+        uint32_t it = 0, done = 0;
+        for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++done) {
+            const uint32_t steps = wide_unit<BT>(u, P).steps;
+            ok = __all_sync(kFull, mbar_wait(&sums_empty, (done & 1) ^ 1));
+            for (uint32_t k = 0; k < steps && ok; ++k, ++it) {
+                const uint32_t r = it % R;
+                ok = __all_sync(kFull, mbar_wait(&ready[r], (it / R) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const uint8_t *x = widened + r * C::kBytesF;
+                const uint64_t b0 = smem_operand(x, 0), b1 = smem_operand(x + C::kBytesF / 2, 0);
+                if (issues) {
 #pragma unroll
                     for (int j = 0; j < kStepK / 16; ++j)
-                        mma_tmem(tmem, tmem + C::kFirstA + r * kACols + 8 * j, (j < 4 ? b0 : b1) + (j & 3) * 2, kInstr,
-                                 k > 0 || j > 0);
+                        mma_tmem(0, C::kFirstA + r * kACols + 8 * j, (j < 4 ? b0 : b1) + (j & 3) * 2, kInstr, k > 0 || j > 0);
                     mma_commit(&freed[r]);
                 }
-                mma_commit(&sums_full);
+                __syncwarp();
             }
+            if (issues && ok) mma_commit(&sums_full);
+            __syncwarp();
         }
     } else if (warp >= 4) {
         const uint32_t group = (warp - 4) >> 2;
         const int quarter = warp & 3, row = quarter * 32 + lane;
-        const uint32_t mine = tmem + (static_cast<uint32_t>(quarter * 32) << 16);  // the warp's lanes of tensor memory
+        const uint32_t mine = static_cast<uint32_t>(quarter * 32) << 16;  // the warp's lanes of tensor memory
         uint32_t it = 0, done = 0;
         for (uint32_t u = blockIdx.x; u < units && ok; u += gridDim.x, ++done) {
             const WideUnit w = wide_unit<BT>(u, P);
@@ -276,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (warp == 1) {
         __syncwarp();
-        tmem_free<kTmemCols>(tmem);
+        tmem_free<kTmemCols>(0);
     }
 }
 

@@ -9,6 +9,24 @@
 
 namespace qc {
 
+// ---------------------------------------------------------------- one thread
+
+// The warp's index as a value that the compiler knows to be the same in every lane:
+// what depends on it alone (addresses, descriptors) then stays in uniform
+// registers, where the tensor instructions take their operands from.
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0); }
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool one_lane() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // ------------------------------------------------------------------ clusters
 
 __device__ __forceinline__ uint32_t cluster_rank() {
