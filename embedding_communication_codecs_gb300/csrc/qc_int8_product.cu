@@ -39,6 +39,7 @@ constexpr int kBlockM = 128;    // rows of A per block
 constexpr int kPairM = 2 * kBlockM;
 constexpr int kStoreWarps = 8;
 constexpr int kGemmThreads = 32 * (2 + kStoreWarps);
+constexpr int kTmemCols = 512;  // all of tensor memory, so it starts at column 0
 constexpr int kGroupM = 8;      // tiles along M that share their B tiles in L2
 // The tensor core's running sum loses up to a unit in the last place per
 // instruction, always towards zero, so its error grows with the length of the sum
@@ -52,7 +53,6 @@ struct Tile {
     static constexpr int kBytesA = kBlockM * kStep * 2, kBytesB = kRowsB * kStep * 2;
     static constexpr int kStage = kBytesA + kBytesB;
     static constexpr int kStages = BN == 256 ? 6 : 8;
-    static constexpr int kTmemCols = 2 * BN;
     static constexpr int kWarpCols = BN / 2;               // columns of a storing warp
     static constexpr int kSmem = kStages * kStage + kStoreWarps * 4096 + 1024;  // tiles start on 1024 bytes
 };
@@ -220,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     __shared__ uint64_t full[S], empty[S], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_slot;
     uint8_t *const tiles = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform_warp(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t tiles_m = static_cast<uint32_t>((P.M + kPairM - 1) / kPairM);
     const uint32_t tiles_n = static_cast<uint32_t>((P.N + BN - 1) / BN);
@@ -238,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         mbar_init(&drained, 1);
         fence_barrier_init();
     }
-    if (warp == 1) tmem_alloc_pair<T::kTmemCols>(&tmem_slot);
+    if (warp == 1) tmem_alloc_pair<kTmemCols>(&tmem_slot);
     if (threadIdx.x == 0) {
         prefetch_map(&map_a);
         prefetch_map(&map_b);
@@ -247,7 +247,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
     bool ok = true;
 
     if (warp == 0) {
@@ -287,38 +286,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 for (uint32_t i = it > S ? it - S : 0; i < it; ++i) ok &= mbar_wait_cluster(&full[i % S], (i / S) & 1);
         }
     } else if (warp == 1) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            // the whole warp goes round, one lane issues
             constexpr uint32_t kInstr = bf16_instruction(kPairM, BN, A_MN, B_MN);
             // 16 contraction elements on: 32 bytes inside a row, or 16 rows of 128 bytes
             constexpr uint32_t kNextA = (A_MN ? 2048 : 32) >> 4, kNextB = (B_MN ? 2048 : 32) >> 4;
+            const bool issues = one_lane();
             uint32_t it = 0, part = 0;  // parts so far: the two sums in tensor memory are used in turn
             for (uint32_t u = pair; u < units && ok; u += npairs) {
                 const uint32_t steps = unit_at(u, tiles_m, tiles_n, P).steps;
                 for (uint32_t k0 = 0; k0 < steps && ok; k0 += kPartSteps, ++part) {
                     const uint32_t buf = part & 1, k1 = min(k0 + kPartSteps, steps);
-                    if (!mbar_wait_cluster(&sums_empty[buf], ((part >> 1) & 1) ^ 1)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(kFull, mbar_wait_cluster(&sums_empty[buf], ((part >> 1) & 1) ^ 1));
+                    if (!ok) break;
                     tc_fence_after();
                     for (uint32_t k = k0; k < k1; ++k, ++it) {
                         const uint32_t s = it % S;
-                        if (!mbar_wait_cluster(&full[s], (it / S) & 1)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = __all_sync(kFull, mbar_wait_cluster(&full[s], (it / S) & 1));
+                        if (!ok) break;
                         tc_fence_after();
                         const uint64_t a = smem_operand(tiles + s * T::kStage, 64 * kStep * 2);
                         const uint64_t b = smem_operand(tiles + s * T::kStage + T::kBytesA, 64 * kStep * 2);
+                        if (issues) {
 #pragma unroll
-                        for (int j = 0; j < kStep / 16; ++j)
-                            mma_pair(tmem + buf * BN, a + j * kNextA, b + j * kNextB, kInstr, k > k0 || j > 0);
-                        mma_commit_pair(&empty[s]);
+                            for (int j = 0; j < kStep / 16; ++j)
+                                mma_pair(buf * BN, a + j * kNextA, b + j * kNextB, kInstr, k > k0 || j > 0);
+                            mma_commit_pair(&empty[s]);
+                        }
+                        __syncwarp();
                     }
-                    mma_commit_pair(&sums_full[buf]);
+                    if (issues) mma_commit_pair(&sums_full[buf]);
+                    __syncwarp();
                 }
             }
-            mma_commit_pair(&drained);
+            if (issues) mma_commit_pair(&drained);
+            __syncwarp();
         }
         // neither block leaves before the leading block's last instruction and the
         // arrivals that it sent to both blocks
@@ -326,7 +328,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     } else {
         const int quarter = warp & 3;                         // the 32 lanes of tensor memory that this warp may read
         const uint32_t c0 = (warp - 2) / 4 * T::kWarpCols;    // its half of the columns
-        const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+        const uint32_t from = (static_cast<uint32_t>(quarter * 32) << 16) + c0;
         uint8_t *const buf = tiles + S * T::kStage + (warp - 2) * 4096;
         uint32_t part = 0;
         for (uint32_t u = pair; u < units && ok; u += npairs) {
@@ -359,7 +361,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     tc_fence_before();
     __syncthreads();
     cluster_sync();
-    if (warp == 1) tmem_free_pair<T::kTmemCols>(tmem);
+    if (warp == 1) tmem_free_pair<kTmemCols>(0);
 }
 
 // Four columns of a row per thread.
