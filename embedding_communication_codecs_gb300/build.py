@@ -21,7 +21,7 @@ SOURCES = ["qc_api.cu", "qc_encode.cu", "qc_encode_tma.cu", "qc_encode_clip.cu",
            "qc_encode_clip_bf16.cu", "qc_encode_bf16.cu", "qc_encode_bf16_fast.cu", "qc_decode.cu", "qc_decode_tma.cu",
            "qc_reencode.cu", "qc_reencode_other.cu", "qc_topk.cu", "qc_fp8.cu",
            "qc_encode_log.cu", "qc_reencode_log.cu", "qc_selftest.cu", "qc_encode_direct_log.cu",
-           "qc_api_layer.cu", "qc_int8_rows.cu", "qc_int8_product.cu", "qc_int8_few.cu", "qc_int8_wide.cu"]
+           "qc_api_layer.cu", "qc_int8_rows.cu", "qc_int8_product.cu", "qc_int8_few.cu", "qc_int8_wide.cu", "qc_int8_ragged.cu"]
 HEADERS = ["qc_device.cuh", "qc_internal.h", "qc_encode_math.cuh", "qc_encode_tma.cuh",
            "qc_encode_direct.cuh",
            "qc_reencode.cuh", "qc_pipeline.cuh", "qc_decode_math.cuh", "qc_exact_norm.cuh",

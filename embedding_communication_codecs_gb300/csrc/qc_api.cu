@@ -342,7 +342,7 @@ qc_status qc_take_device_errors(uint32_t *flags) {
         qc::take_reencode_other_errors,  qc::take_encode_log_errors,  qc::take_reencode_log_errors,
         qc::take_selftest_errors,        qc::take_topk_errors,        qc::take_encode_bf16_errors,
         qc::take_encode_bf16_fast_errors, qc::take_decode_errors,     qc::take_reencode_errors,
-        qc::take_product_errors,        qc::take_wide_errors};
+        qc::take_product_errors,        qc::take_wide_errors,         qc::take_gate_errors};
     uint32_t all = 0;
     for (auto take : takes) {
         uint32_t v = 0;

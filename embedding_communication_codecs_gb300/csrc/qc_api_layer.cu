@@ -175,6 +175,7 @@ qc_status qc_swiglu_encode(const void *gate_up, qc_dtype dtype, size_t stride, s
     p.h_scale = h_scale;
     p.saved_codes = saved_codes;
     p.saved_scale = saved_scale;
+    p.status = qc::api::status_word();
     return from_cuda(qc::launch_swiglu_encode(p, dtype == QC_DTYPE_BF16, stream_of(stream)), fn);
 }
 

@@ -85,12 +85,6 @@ __device__ __forceinline__ Unit unit_at(uint32_t u, uint32_t tiles_m, uint32_t t
     return {g * kGroupM + r % rows, r / rows, split, first, min(P.split_steps, all - first)};
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // Adds a storing warp's C columns of tensor memory to its registers.
 template <int C>
 __device__ __forceinline__ void add_sums(uint32_t at, float (&acc)[C]) {

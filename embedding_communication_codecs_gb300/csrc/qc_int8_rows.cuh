@@ -40,6 +40,12 @@ __device__ __forceinline__ float clamp_to_cap(float x) { return fminf(fmaxf(x, -
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
+// The larger of m and |x|, a NaN if either is one.
+__device__ __forceinline__ float max_magnitude(float m, float x) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x)));
+    return m;
+}
+
 // rint(x * inverse), ties to even, in the low byte (two's complement): the exact
 // product plus 1.5 * 2^23 leaves the integer in the low mantissa bits.  A row
 // whose codes are all 0 has inverse 0; an infinity or NaN there is masked.
@@ -59,9 +65,190 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
     return r;
 }
 
+// Two of them in a word, `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 __device__ __forceinline__ float load_as_float(const float *p) { return *p; }
 __device__ __forceinline__ float load_as_float(const uint16_t *p) { return bf16_bits_to_float(*p); }
 __device__ __forceinline__ void store_from_float(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_from_float(uint16_t *p, float x) { *p = to_bf16(x); }
+
+
+constexpr int kRowThreads = 256;
+
+// U consecutive elements of a row, as they lie in memory: fp32 values, or pairs of
+// bf16 in words (a word's halves become fp32 by one shift or mask each).
+template <int U>
+struct alignas(U * 4 > 16 ? 16 : U * 4) RawF32 {
+    float v[U];
+    __device__ __forceinline__ float get(int j) const { return v[j]; }
+    __device__ __forceinline__ void set(int j, float x) { v[j] = x; }
+    __device__ __forceinline__ void set_all(const float (&x)[U]) {
+#pragma unroll
+        for (int j = 0; j < U; ++j) v[j] = x[j];
+    }
+};
+template <int U>
+struct alignas(U * 2 > 16 ? 16 : U * 2) RawBf16 {
+    uint32_t w[U / 2];
+    __device__ __forceinline__ float get(int j) const {
+        return __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+    }
+    // in order of j
+    __device__ __forceinline__ void set(int j, uint16_t x) {
+        w[j / 2] = j & 1 ? w[j / 2] | static_cast<uint32_t>(x) << 16 : static_cast<uint32_t>(x);
+    }
+    __device__ __forceinline__ void set_all(const float (&x)[U]) {
+#pragma unroll
+        for (int j = 0; j < U; j += 2) w[j / 2] = pack_bf16(x[j], x[j + 1]);
+    }
+};
+template <>
+struct RawBf16<1> {
+    uint16_t v;
+    __device__ __forceinline__ float get(int) const { return bf16_bits_to_float(v); }
+    __device__ __forceinline__ void set_all(const float (&x)[1]) { v = to_bf16(x[0]); }
+};
+
+// The largest magnitude pattern of a unit, as an fp32 pattern.
+template <int U>
+__device__ __forceinline__ uint32_t unit_max(const RawF32<U> &r, uint32_t m) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) m = max(m, abs_bits(r.v[j]));
+    return m;
+}
+// bf16 patterns order like fp32 ones: pairs of them are compared at once.
+template <int U>
+__device__ __forceinline__ uint32_t unit_max(const RawBf16<U> &r, uint32_t m) {
+    uint32_t p = r.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int j = 1; j < U / 2; ++j) p = __vmaxu2(p, r.w[j] & 0x7FFF7FFFu);
+    return max(m, max(p & 0xFFFF0000u, p << 16));
+}
+
+template <typename T, int U>
+struct RawOf;
+template <int U>
+struct RawOf<float, U> {
+    using type = RawF32<U>;
+};
+template <int U>
+struct RawOf<uint16_t, U> {
+    using type = RawBf16<U>;
+};
+
+template <typename T, int U>
+__device__ __forceinline__ typename RawOf<T, U>::type load_unit(const T *p) {
+    return *reinterpret_cast<const typename RawOf<T, U>::type *>(p);
+}
+
+// The codes of U elements, four to a word.
+template <int U>
+__device__ __forceinline__ void store_codes(int8_t *p, const uint32_t (&c)[U]) {
+    if constexpr (U == 1) {
+        *p = static_cast<int8_t>(c[0] & 0xFFu);
+    } else {
+        static_assert(U == 8, "a unit is 8 bytes of codes");
+        *reinterpret_cast<uint2 *>(p) =
+            make_uint2(pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7]));
+    }
+}
+
+// U fp32 values rounded to the output's type.
+template <typename T, int U>
+__device__ __forceinline__ void store_values(T *p, const float (&v)[U]) {
+    typename RawOf<T, U>::type r;
+    r.set_all(v);
+    *reinterpret_cast<typename RawOf<T, U>::type *>(p) = r;
+}
+
+// A team of `lanes` threads (a power of two, 8 to THREADS) and the rows it owns.
+struct Team {
+    uint32_t lanes, lane, first, stride;
+    __device__ explicit Team(uint32_t lanes_) : lanes(lanes_) {
+        const uint32_t teams = blockDim.x / lanes;
+        lane = threadIdx.x & (lanes - 1);
+        first = blockIdx.x * teams + threadIdx.x / lanes;
+        stride = gridDim.x * teams;
+    }
+};
+
+// The largest of v[0..N) over the team, in every lane.  A team of several warps
+// meets in shared memory, in one of two buffers used in turn, so one block barrier
+// a row is enough; every thread of the block takes part.
+template <int N>
+__device__ __forceinline__ void team_max(uint32_t (&v)[N], uint32_t lanes, uint32_t (*red)[32][N], int &turn) {
+    for (uint32_t o = min(lanes, 32u) >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = max(v[i], __shfl_xor_sync(kFull, v[i], o));
+    if (lanes > 32) {
+        const uint32_t warp = threadIdx.x >> 5, w0 = threadIdx.x / lanes * (lanes >> 5);
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[turn][warp][i] = v[i];
+        __syncthreads();
+        for (uint32_t w = 0; w < (lanes >> 5); ++w)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = max(v[i], red[turn][w0 + w][i]);
+        turn ^= 1;
+    }
+}
+
+// Codes of U elements under a scale that neither zeroes nor saturates them.
+template <int U, typename Get>
+__device__ __forceinline__ void encode_unit(int8_t *out, float inverse, Get get) {
+    uint32_t c[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) c[j] = code_bits(get(j), inverse);
+    store_codes<U>(out, c);
+}
+
+// U codes as they lie in memory.  A code becomes a float without a conversion
+// instruction (those run at a quarter of the rate): its byte, offset by 128, under
+// the exponent of 2^23, minus 2^23 + 128.
+template <int U>
+struct alignas(U) RawCodes {
+    uint32_t w[U / 4];
+    __device__ __forceinline__ float get(int j) const {
+        return __fsub_rn(__uint_as_float(__byte_perm(w[j / 4] ^ 0x80808080u, 0x4B000000u, 0x7440 + (j & 3))), 8388736.0f);
+    }
+};
+template <>
+struct RawCodes<1> {
+    int8_t b;
+    __device__ __forceinline__ float get(int) const { return static_cast<float>(b); }
+};
+
+// 1 / (1 + exp(-g)) by the hardware's exponential (base 2) and reciprocal: their
+// errors and the argument's rounding (|g| half units) stay below 2^-19 relative for
+// |g| < 16, an eighth of a per cent of half a code's step.  Saturates to 1 and 0.
+__device__ __forceinline__ float sigmoid(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.4426950408889634f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
+    return r;
+}
+
+__device__ __forceinline__ float swiglu(float g, float u) { return __fmul_rn(__fmul_rn(g, sigmoid(g)), u); }
+
+// Lanes of a team that covers `units` with up to V units per lane: 8 to `most`.
+inline uint32_t lanes_for(uint32_t units, int v, uint32_t most) {
+    uint32_t lanes = 8;
+    while (lanes < most && lanes * v < units) lanes *= 2;
+    return lanes;
+}
+
+template <typename P>
+cudaError_t launch_rows(void (*kernel)(const P, uint32_t), const P &p, uint32_t lanes, int threads,
+                        cudaStream_t stream) {
+    const uint64_t teams = threads / lanes;
+    const int grid = persistent_grid(reinterpret_cast<const void *>(kernel), threads, (p.rows + teams - 1) / teams);
+    kernel<<<grid, threads, 0, stream>>>(p, lanes);
+    return cudaGetLastError();
+}
 
 }  // namespace qc

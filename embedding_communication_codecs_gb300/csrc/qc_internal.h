@@ -326,12 +326,18 @@ struct SwigluParams {
     const float *saved_scale_in;
     void *dgate_up;
     uint64_t dgate_up_stride;
+    uint32_t *status;
 };
 
 cudaError_t launch_rows_int8_encode(const RowCodesParams &p, int bf16, cudaStream_t stream);
 cudaError_t launch_rows_int8_decode(const RowCodesParams &p, int bf16, cudaStream_t stream);
 cudaError_t launch_swiglu_encode(const SwigluParams &p, int bf16, cudaStream_t stream);
 cudaError_t launch_swiglu_backward(const SwigluParams &p, int bf16, cudaStream_t stream);
+
+// The same for rows that start anywhere (qc_int8_ragged.cu).
+cudaError_t launch_ragged_encode(const RowCodesParams &p, int bf16, cudaStream_t stream);
+cudaError_t launch_ragged_decode(const RowCodesParams &p, int bf16, cudaStream_t stream);
+cudaError_t launch_ragged_swiglu_encode(const SwigluParams &p, int bf16, cudaStream_t stream);
 
 // One product of the layer: out[M, N] = sum over L of the operands named per launcher.
 struct ProductParams {
@@ -407,6 +413,7 @@ cudaError_t take_encode_bf16_fast_errors(uint32_t *flags);
 cudaError_t take_decode_errors(uint32_t *flags);
 cudaError_t take_product_errors(uint32_t *flags);
 cudaError_t take_wide_errors(uint32_t *flags);
+cudaError_t take_gate_errors(uint32_t *flags);
 cudaError_t take_reencode_errors(uint32_t *flags);
 
 }  // namespace qc
