@@ -3,8 +3,10 @@
 // with units of eight elements laid on the output's 8- or 16-byte boundaries, so that
 // stores stay vectors.  The input, which then starts anywhere, is read as the aligned
 // vectors around a unit and shifted in registers; one element at a time (a load and a
-// byte store per element) 16384 x 8191 bf16 took 221 us to encode, this XX.  Vectors
+// byte store per element) 16384 x 8191 bf16 took 221 us to encode, this 117.  Vectors
 // that reach outside the matrix are not read: those units load single elements.
+#include <algorithm>
+
 #include "qc_int8_rows.cuh"
 #include "qc_internal.h"
 
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ragged_swiglu_encode(const Swi
         int8_t *saved = P.saved_codes + (live ? r : 0) * 2 * P.dim, *out = P.h_codes + (live ? r : 0) * P.dim;
         const int step = 8 * static_cast<int>(lanes), lane8 = 8 * static_cast<int>(team.lane);
         uint32_t m[3] = {0, 0, 0};
-#pragma unroll 2
+#pragma unroll 1
         for (int e = lane8 - phase8(saved); e < dim; e += step) {
             const auto g = load8_any<ALIGNED>(gate, e, dim, begin, end);
             const auto w = load8_any<false>(up, e, dim, begin, end);
@@ -220,17 +222,17 @@ __global__ void __launch_bounds__(kRowThreads, 4) ragged_swiglu_encode(const Swi
             P.saved_scale[2 * r + 1] = su.scale;
             P.h_scale[r] = sh.scale;
         }
-#pragma unroll 2
+#pragma unroll 1
         for (int e = lane8 - phase8(saved); e < dim; e += step) {
             const auto g = load8_any<ALIGNED>(gate, e, dim, begin, end);
             encode_any(saved, e, dim, sg, [&](int j) { return g.get(j); });
         }
-#pragma unroll 2
+#pragma unroll 1
         for (int e = lane8 - phase8(saved + dim); e < dim; e += step) {
             const auto w = load8_any<ALIGNED>(up, e, dim, begin, end);
             encode_any(saved + dim, e, dim, su, [&](int j) { return w.get(j); });
         }
-#pragma unroll 2
+#pragma unroll 1
         for (int e = lane8 - phase8(out); e < dim; e += step) {
             const auto g = load8_any<false>(gate, e, dim, begin, end), w = load8_any<false>(up, e, dim, begin, end);
             encode_any(out, e, dim, sh, [&](int j) { return swiglu(g.get(j), w.get(j)); });
@@ -243,14 +245,24 @@ bool in_step(const void *x, uint64_t x_stride, size_t esize, const void *codes, 
     return x_stride == dim && reinterpret_cast<uintptr_t>(x) % (8 * esize) == reinterpret_cast<uintptr_t>(codes) % 8 * esize;
 }
 
+// Lanes of a team that goes over its row several times, about `most` units to a lane.
+// A team of one warp meets without a block barrier, and a row's two ends, which load
+// single elements, hold up fewer warps: 16384 x 4099 fp32 takes 76 us to encode with 32
+// lanes to a row and 101 with enough lanes to hold it.  With few rows, more lanes each.
+uint32_t few_lanes(uint32_t units, int most, uint64_t rows) {
+    uint32_t lanes = lanes_for(units, most, kRowThreads);
+    while (lanes < kRowThreads && lanes < units && rows * lanes < 152 * 512) lanes *= 2;
+    return lanes;
+}
+
 template <typename T, bool ALIGNED>
 cudaError_t encode(const RowCodesParams &p, cudaStream_t stream) {
     const uint32_t units = (p.dim + 14) / 8;  // at the worst phase
     constexpr int kBlocks = sizeof(T) == 2 ? 4 : 3;
     if (units <= 32) return launch_rows(ragged_encode<T, ALIGNED, 1, true, 6>, p, lanes_for(units, 1, 32), kRowThreads, stream);
-    if (units <= 4 * kRowThreads)
+    if (units <= 128 || (p.rows < 8 * 304 && units <= 4 * kRowThreads))
         return launch_rows(ragged_encode<T, ALIGNED, 4, true, kBlocks>, p, lanes_for(units, 4, kRowThreads), kRowThreads, stream);
-    return launch_rows(ragged_encode<T, ALIGNED, 4, false, kBlocks>, p, kRowThreads, kRowThreads, stream);
+    return launch_rows(ragged_encode<T, ALIGNED, 4, false, kBlocks>, p, std::max(32u, few_lanes(units, 36, p.rows)), kRowThreads, stream);
 }
 
 template <typename T>
@@ -272,7 +284,7 @@ cudaError_t launch_ragged_decode(const RowCodesParams &p, int bf16, cudaStream_t
 }
 
 cudaError_t launch_ragged_swiglu_encode(const SwigluParams &p, int bf16, cudaStream_t stream) {
-    const uint32_t lanes = lanes_for((p.dim + 14) / 8, 2, kRowThreads);
+    const uint32_t lanes = few_lanes((p.dim + 14) / 8, 9, p.rows);
     const bool aligned = in_step(p.in, p.in_stride, bf16 ? 2 : 4, p.saved_codes, 2 * static_cast<uint64_t>(p.dim));
     const auto kernel = bf16 ? aligned ? ragged_swiglu_encode<uint16_t, true> : ragged_swiglu_encode<uint16_t, false>
                              : aligned ? ragged_swiglu_encode<float, true> : ragged_swiglu_encode<float, false>;
