@@ -1,4 +1,5 @@
-"""Build libqcodec.so in-tree with nvcc for sm_103a.
+"""Build libqcodec.so in-tree with nvcc for sm_103a, and the torch binding of the
+8-bit layer's calls (``_qcbind``) next to it with g++.
 
 Each CUDA translation unit is compiled to an object file in parallel, then the
 objects are linked into a shared library next to this file.  The CUDA runtime
@@ -17,6 +18,8 @@ ROOT = os.path.dirname(PKG)
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libqcodec.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+BIND_PATH = os.path.join(PKG, "_qcbind.so")
+BIND_SOURCE = "qc_bind.cpp"
 SOURCES = ["qc_api.cu", "qc_encode.cu", "qc_encode_tma.cu", "qc_encode_clip.cu",
            "qc_encode_clip_bf16.cu", "qc_encode_bf16.cu", "qc_encode_bf16_fast.cu", "qc_decode.cu", "qc_decode_tma.cu",
            "qc_reencode.cu", "qc_reencode_other.cu", "qc_topk.cu", "qc_fp8.cu",
@@ -42,17 +45,31 @@ def nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BIND_SOURCE]]
     files.append(os.path.join(ROOT, "include", "qcodec.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not (os.path.exists(LIB_PATH) and os.path.exists(BIND_PATH)):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BIND_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def bind_flags():
+    """Compiler and linker flags of an extension against the installed torch."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               cuda, sysconfig.get_paths()["include"]]
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return ([f"-D_GLIBCXX_USE_CXX11_ABI={abi}"] + [f"-I{p}" for p in include],
+            [f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
 
 
 def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -71,18 +88,36 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool =
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    def compile_bind():
+        obj = os.path.join(BUILD_DIR, "qc_bind.o")
+        flags, libs = bind_flags()
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *flags, "-c", os.path.join(CSRC, BIND_SOURCE), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {BIND_SOURCE}:\n{r.stdout}\n{r.stderr}")
+        return obj, libs
+
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        bind = ex.submit(compile_bind)
         results = list(ex.map(compile_one, SOURCES))
+        bind_obj, bind_libs = bind.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log:
                 print(log)
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-cudart", "static"]
+    cmd = [cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-cudart", "static",
+           "-Xlinker", f"-soname={LIB_NAME}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, bind_obj, LIB_PATH, "-Wl,-rpath,$ORIGIN", *bind_libs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND_PATH)
     return LIB_PATH
 
 

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import torch
 
+from . import _qcbind
 from . import (QC_ACCUMULATE_INTO_OUT, QC_DTYPE_BF16, QC_DTYPE_F32, _check, _need, _on_device, _ptr,
                _stream, lib)
 
@@ -157,12 +158,10 @@ def qc_swiglu_backward(dh, dtype, dh_stride, saved_codes, saved_scale, rows, dim
 
 # -------------------------------------------------------------- conveniences
 #
-# Each call first asks, in one expression, whether its tensors are plainly right
-# (dense, of the expected types and shapes, on a CUDA device); only if not does it
-# look closer, to accept a strided matrix or to say what is wrong.  For a call of a
-# few microseconds on the GPU, the host's time is what counts.
-
-_empty = torch.empty
+# Plainly right arguments (dense tensors of the expected types and shapes on a CUDA
+# device) go through the compiled binding, which allocates and calls the library
+# without Python in between.  Where it declines (None), the code here looks closer:
+# it accepts a strided matrix and says what is wrong with anything else.
 
 
 def _rows(t, name, dtypes):
@@ -196,19 +195,6 @@ def _codes(codes, scale, what):
     _dense(scale, f"{what}_scale", _F32, (shape[0],))
 
 
-def _plain_codes(codes, scale):
-    """Dense row codes and scales on a CUDA device."""
-    return (isinstance(codes, torch.Tensor) and isinstance(scale, torch.Tensor) and codes.dim() == 2
-            and codes.dtype is torch.int8 and scale.dtype is torch.float32 and scale.shape == codes.shape[:1]
-            and codes.is_contiguous() and scale.is_contiguous() and codes.is_cuda and scale.is_cuda)
-
-
-def _plain_rows(t):
-    """A dense fp32 or bf16 matrix on a CUDA device."""
-    return (isinstance(t, torch.Tensor) and t.dim() == 2 and t.dtype in _CODE_OF and t.is_contiguous()
-            and t.is_cuda)
-
-
 def _dtype(dtype):
     if dtype not in _CODE_OF:
         raise ValueError(f"dtype {dtype} is not torch.float32 or torch.bfloat16")
@@ -229,6 +215,21 @@ def _current(t):
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _done(got):
+    """What the binding answered: results, or the status of a call that failed."""
+    if type(got) is int:
+        _check(got)
+    return got
+
+
+def _empty(like, *shape, dtype):
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _scratch(like, nbytes):
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
+
+
 def rowwise_int8(x, *, stream=None):
     """int8 codes of x's shape and one fp32 power-of-two scale per row.
 
@@ -236,19 +237,16 @@ def rowwise_int8(x, *, stream=None):
     if stream is not None:
         with _on(stream):
             return rowwise_int8(x)
-    if _plain_rows(x):
-        stride = x.shape[1]
-    else:
-        stride = _rows(x, "x", _CODE_OF)
-        _on_device(x=x)
+    got = _qcbind.rowwise_int8(x)
+    if got is not None:
+        return _done(got)
+    stride = _rows(x, "x", _CODE_OF)
+    _on_device(x=x)
     rows, dim = x.shape
-    device = x.device
-    codes = _empty((rows, dim), dtype=torch.int8, device=device)
-    scale = _empty((rows,), dtype=torch.float32, device=device)
-    status = lib.qc_rowwise_int8(x.data_ptr(), _CODE_OF[x.dtype], stride, rows, dim, codes.data_ptr(),
-                                 scale.data_ptr(), _current(x))
-    if status:
-        _check(status)
+    codes = _empty(x, rows, dim, dtype=torch.int8)
+    scale = _empty(x, rows, dtype=torch.float32)
+    _check(lib.qc_rowwise_int8(x.data_ptr(), _CODE_OF[x.dtype], stride, rows, dim, codes.data_ptr(),
+                               scale.data_ptr(), _current(x)))
     return codes, scale
 
 
@@ -257,17 +255,13 @@ def rowwise_int8_dequant(codes, row_scale, *, dtype=torch.bfloat16, stream=None)
     if stream is not None:
         with _on(stream):
             return rowwise_int8_dequant(codes, row_scale, dtype=dtype)
-    code = _dtype(dtype)
-    if not _plain_codes(codes, row_scale):
-        _codes(codes, row_scale, "row")
-        _on_device(codes=codes, row_scale=row_scale)
-    rows, dim = codes.shape
-    out = _empty((rows, dim), dtype=dtype, device=codes.device)
-    status = lib.qc_rowwise_int8_dequant(codes.data_ptr(), row_scale.data_ptr(), rows, dim, out.data_ptr(),
-                                         code, dim, _current(codes))
-    if status:
-        _check(status)
-    return out
+    _dtype(dtype)
+    got = _qcbind.rowwise_int8_dequant(codes, row_scale, dtype is torch.bfloat16)
+    if got is not None:
+        return _done(got)
+    _codes(codes, row_scale, "row")
+    _on_device(codes=codes, row_scale=row_scale)
+    raise ValueError("codes and row_scale are not usable")
 
 
 def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bfloat16, stream=None):
@@ -276,36 +270,18 @@ def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bf
     if stream is not None:
         with _on(stream):
             return int8_matmul(x_codes, x_scale, w_codes, w_scale, bias, dtype=dtype)
-    code = _dtype(dtype)
-    plain = _plain_codes(x_codes, x_scale) and _plain_codes(w_codes, w_scale)
-    if not plain:
-        _codes(x_codes, x_scale, "x")
-        _codes(w_codes, w_scale, "w")
+    _dtype(dtype)
+    got = _qcbind.int8_matmul(x_codes, x_scale, w_codes, w_scale, bias, dtype is torch.bfloat16)
+    if got is not None:
+        return _done(got)
+    _codes(x_codes, x_scale, "x")
+    _codes(w_codes, w_scale, "w")
     if bias is not None:
         _dense(bias, "bias", _F32, (w_codes.shape[0],))
-        plain = plain and bias.is_cuda
-    T, K = x_codes.shape
-    N, kw = w_codes.shape
-    if kw != K:
-        raise ValueError(f"w_codes has rows of {kw}, x_codes of {K}")
-    device = x_codes.device
-    if not plain:
-        _on_device(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias)
-    y = _empty((T, N), dtype=dtype, device=device)
-    nbytes = lib.qc_int8_matmul_workspace(T, N, K)
-    ws = _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    status = lib.qc_int8_matmul(x_codes.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
-                                w_scale.data_ptr(), None if bias is None else bias.data_ptr(), T, N, K,
-                                y.data_ptr(), code, N, ws.data_ptr() if nbytes else None, nbytes,
-                                _current(x_codes))
-    if status:
-        _check(status)
-    return y
-
-
-def _plain_dy(dy):
-    return (isinstance(dy, torch.Tensor) and dy.dim() == 2 and dy.dtype is torch.bfloat16
-            and dy.is_contiguous() and dy.is_cuda)
+    if w_codes.shape[1] != x_codes.shape[1]:
+        raise ValueError(f"w_codes has rows of {w_codes.shape[1]}, x_codes of {x_codes.shape[1]}")
+    _on_device(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias)
+    raise ValueError("the tensors are not usable")
 
 
 def int8_input_grad(dy, w_codes, w_scale, *, dtype=torch.bfloat16, stream=None):
@@ -314,25 +290,21 @@ def int8_input_grad(dy, w_codes, w_scale, *, dtype=torch.bfloat16, stream=None):
         with _on(stream):
             return int8_input_grad(dy, w_codes, w_scale, dtype=dtype)
     code = _dtype(dtype)
-    plain = _plain_codes(w_codes, w_scale) and _plain_dy(dy)
-    if not plain:
-        _codes(w_codes, w_scale, "w")
-        _rows(dy, "dy", _BF16)
-    N, K = w_codes.shape
+    got = _qcbind.int8_input_grad(dy, w_codes, w_scale, dtype is torch.bfloat16)
+    if got is not None:
+        return _done(got)
+    _codes(w_codes, w_scale, "w")
+    stride = _rows(dy, "dy", _BF16)
     T, n = dy.shape
+    N, K = w_codes.shape
     if n != N:
         raise ValueError(f"dy has rows of {n}, w_codes has {N} rows")
-    if not plain:
-        _on_device(dy=dy, w_codes=w_codes, w_scale=w_scale)
-    device = dy.device
-    dx = _empty((T, K), dtype=dtype, device=device)
+    _on_device(dy=dy, w_codes=w_codes, w_scale=w_scale)
+    dx = _empty(dy, T, K, dtype=dtype)
     nbytes = lib.qc_int8_input_grad_workspace(T, N, K)
-    ws = _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    status = lib.qc_int8_input_grad(dy.data_ptr(), dy.stride(0) if T > 1 else N, w_codes.data_ptr(),
-                                    w_scale.data_ptr(), T, N, K, dx.data_ptr(), code, K,
-                                    ws.data_ptr() if nbytes else None, nbytes, _current(dy))
-    if status:
-        _check(status)
+    ws = _scratch(dy, nbytes)
+    _check(lib.qc_int8_input_grad(dy.data_ptr(), stride, w_codes.data_ptr(), w_scale.data_ptr(), T, N, K,
+                                  dx.data_ptr(), code, K, _ptr(ws), nbytes, _current(dy)))
     return dx
 
 
@@ -344,10 +316,13 @@ def int8_weight_grad(dy, x_codes, x_scale, *, dtype=torch.float32, with_bias=Fal
     if stream is not None:
         with _on(stream):
             return int8_weight_grad(dy, x_codes, x_scale, dtype=dtype, with_bias=with_bias, into=into)
-    plain = _plain_codes(x_codes, x_scale) and _plain_dy(dy)
-    if not plain:
-        _codes(x_codes, x_scale, "x")
-        _rows(dy, "dy", _BF16)
+    if into is None:
+        _dtype(dtype)
+        got = _qcbind.int8_weight_grad(dy, x_codes, x_scale, dtype is torch.bfloat16, bool(with_bias))
+        if got is not None:
+            return _done(got)
+    _codes(x_codes, x_scale, "x")
+    stride = _rows(dy, "dy", _BF16)
     T, K = x_codes.shape
     t, N = dy.shape
     if t != T:
@@ -359,22 +334,16 @@ def int8_weight_grad(dy, x_codes, x_scale, *, dtype=torch.float32, with_bias=Fal
         if dbias is not None:
             _dense(dbias, "dbias", _F32, (N,))
         _on_device(dw=dw, dbias=dbias)
-    code = _dtype(dtype)
-    if not plain:
-        _on_device(dy=dy, x_codes=x_codes, x_scale=x_scale)
-    device = dy.device
+    _on_device(dy=dy, x_codes=x_codes, x_scale=x_scale)
     if into is None:
-        dw = _empty((N, K), dtype=dtype, device=device)
-        dbias = _empty((N,), dtype=torch.float32, device=device) if with_bias else None
+        dw = _empty(dy, N, K, dtype=dtype)
+        dbias = _empty(dy, N, dtype=torch.float32) if with_bias else None
     nbytes = lib.qc_int8_weight_grad_workspace(T, N, K)
-    ws = _empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    status = lib.qc_int8_weight_grad(dy.data_ptr(), dy.stride(0) if T > 1 else N, x_codes.data_ptr(),
-                                     x_scale.data_ptr(), T, N, K, dw.data_ptr(), code,
-                                     None if dbias is None else dbias.data_ptr(),
-                                     0 if into is None else QC_ACCUMULATE_INTO_OUT,
-                                     ws.data_ptr() if nbytes else None, nbytes, _current(dy))
-    if status:
-        _check(status)
+    ws = _scratch(dy, nbytes)
+    _check(lib.qc_int8_weight_grad(dy.data_ptr(), stride, x_codes.data_ptr(), x_scale.data_ptr(), T, N, K,
+                                   dw.data_ptr(), _CODE_OF[dtype], _ptr(dbias),
+                                   0 if into is None else QC_ACCUMULATE_INTO_OUT, _ptr(ws), nbytes,
+                                   _current(dy)))
     return dw, dbias
 
 
@@ -384,26 +353,21 @@ def swiglu_encode(gate_up, *, stream=None):
     if stream is not None:
         with _on(stream):
             return swiglu_encode(gate_up)
-    if _plain_rows(gate_up):
-        stride = gate_up.shape[1]
-    else:
-        stride = _rows(gate_up, "gate_up", _CODE_OF)
+    got = _qcbind.swiglu_encode(gate_up)
+    if got is not None:
+        return _done(got)
+    stride = _rows(gate_up, "gate_up", _CODE_OF)
     rows, two = gate_up.shape
     if two % 2:
         raise ValueError(f"gate_up has rows of {two}; an even number is needed")
-    device = gate_up.device
-    if device.type != "cuda":
-        _on_device(gate_up=gate_up)
-    dim = two // 2
-    h_codes = _empty((rows, dim), dtype=torch.int8, device=device)
-    h_scale = _empty((rows,), dtype=torch.float32, device=device)
-    saved_codes = _empty((rows, two), dtype=torch.int8, device=device)
-    saved_scale = _empty((rows, 2), dtype=torch.float32, device=device)
-    status = lib.qc_swiglu_encode(gate_up.data_ptr(), _CODE_OF[gate_up.dtype], stride, rows, dim,
-                                  h_codes.data_ptr(), h_scale.data_ptr(), saved_codes.data_ptr(),
-                                  saved_scale.data_ptr(), _current(gate_up))
-    if status:
-        _check(status)
+    _on_device(gate_up=gate_up)
+    h_codes = _empty(gate_up, rows, two // 2, dtype=torch.int8)
+    h_scale = _empty(gate_up, rows, dtype=torch.float32)
+    saved_codes = _empty(gate_up, rows, two, dtype=torch.int8)
+    saved_scale = _empty(gate_up, rows, 2, dtype=torch.float32)
+    _check(lib.qc_swiglu_encode(gate_up.data_ptr(), _CODE_OF[gate_up.dtype], stride, rows, two // 2,
+                                h_codes.data_ptr(), h_scale.data_ptr(), saved_codes.data_ptr(),
+                                saved_scale.data_ptr(), _current(gate_up)))
     return h_codes, h_scale, saved_codes, saved_scale
 
 
@@ -413,18 +377,15 @@ def swiglu_backward(dh, saved_codes, saved_scale, *, stream=None):
     if stream is not None:
         with _on(stream):
             return swiglu_backward(dh, saved_codes, saved_scale)
-    if _plain_rows(dh):
-        stride = dh.shape[1]
-    else:
-        stride = _rows(dh, "dh", _CODE_OF)
+    got = _qcbind.swiglu_backward(dh, saved_codes, saved_scale)
+    if got is not None:
+        return _done(got)
+    stride = _rows(dh, "dh", _CODE_OF)
     rows, dim = dh.shape
     _dense(saved_codes, "saved_codes", _I8, (rows, 2 * dim))
     _dense(saved_scale, "saved_scale", _F32, (rows, 2))
-    if not (dh.is_cuda and saved_codes.is_cuda and saved_scale.is_cuda):
-        _on_device(dh=dh, saved_codes=saved_codes, saved_scale=saved_scale)
-    out = _empty((rows, 2 * dim), dtype=dh.dtype, device=dh.device)
-    status = lib.qc_swiglu_backward(dh.data_ptr(), _CODE_OF[dh.dtype], stride, saved_codes.data_ptr(),
-                                    saved_scale.data_ptr(), rows, dim, out.data_ptr(), 2 * dim, _current(dh))
-    if status:
-        _check(status)
+    _on_device(dh=dh, saved_codes=saved_codes, saved_scale=saved_scale)
+    out = _empty(dh, rows, 2 * dim, dtype=dh.dtype)
+    _check(lib.qc_swiglu_backward(dh.data_ptr(), _CODE_OF[dh.dtype], stride, saved_codes.data_ptr(),
+                                  saved_scale.data_ptr(), rows, dim, out.data_ptr(), 2 * dim, _current(dh)))
     return out
