@@ -28,7 +28,7 @@ SOURCES = ["qc_api.cu", "qc_encode.cu", "qc_encode_tma.cu", "qc_encode_clip.cu",
 HEADERS = ["qc_device.cuh", "qc_internal.h", "qc_encode_math.cuh", "qc_encode_tma.cuh",
            "qc_encode_direct.cuh",
            "qc_reencode.cuh", "qc_pipeline.cuh", "qc_decode_math.cuh", "qc_exact_norm.cuh",
-           "qc_api_util.h", "qc_int8_rows.cuh", "qc_tc.cuh", "qc_tc_host.h"]
+           "qc_api_util.h", "qc_int8_rows.cuh", "qc_tc.cuh", "qc_tc_host.h", "qc_chain.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # -fmad=false: no multiply-add contraction; every fused op is an explicit

@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "qc_chain.cuh"
 #include "qc_int8_rows.cuh"
 #include "qc_internal.h"
 #include "qc_tc.cuh"
@@ -241,6 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    after_previous();
     bool ok = true;
 
     if (warp == 0) {
@@ -468,8 +470,8 @@ cudaError_t launch_gemm(const Operand &a, const Operand &b, const GemmParams &g,
     const uint64_t units = ((g.M + kPairM - 1) / kPairM) * ((g.N + BN - 1) / BN) * g.splits;
     if (units > 0x7FFFFFFFull) return cudaErrorInvalidConfiguration;
     const uint64_t most = sm_count() / 2;  // one block per SM, in pairs
-    kernel<<<static_cast<unsigned>(2 * (units < most ? units : most)), kGemmThreads, T::kSmem, stream>>>(ma, mb, mo, g);
-    return cudaGetLastError();
+    return launch_chained(kernel, static_cast<unsigned>(2 * (units < most ? units : most)), kGemmThreads, T::kSmem, stream, ma, mb,
+                          mo, g);
 }
 
 template <bool A_MN, bool B_MN, Output OUT>
@@ -499,38 +501,36 @@ cudaError_t launch_product(const Operand &a, const Operand &b, GemmParams g, voi
 }
 
 // Column sums of bf16 rows: a cluster of eight blocks owns 32 Q columns, lane l columns
-// Q l .. Q l + Q - 1, and the cluster's 64 warps every 64th row; the warps' fp32 sums
-// are added in order in each block, the blocks' in order by the first.
+// Q l .. Q l + Q - 1, and the cluster's 256 warps every 256th row, eight rows in
+// flight; the warps' fp32 sums are added in order in each block, the blocks' in order
+// by the first.  Loads in flight bound it: 8192 x 4096 takes 20 us, 28 with 64 warps.
 template <int Q>
-__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(256)
+__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(1024)
     column_sums(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t cols, float *out, int accumulate) {
-    __shared__ float sums[8][32 * Q + 1], total[32 * Q];
+    __shared__ float sums[32][32 * Q], total[32 * Q];
+    using R = typename RawOf<uint16_t, Q>::type;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = cluster_rank();
-    const uint64_t c = (static_cast<uint64_t>(blockIdx.x / 8) * 32 + lane) * Q;
+    const uint64_t first = static_cast<uint64_t>(blockIdx.x / 8) * 32 * Q, c = first + lane * Q;
     float s[Q] = {};
     if (c < cols) {
 #pragma unroll 8
-        for (uint64_t r = rank * 8 + warp; r < rows; r += 64) {
-            if constexpr (Q == 2) {
-                const uint32_t v = __ldg(reinterpret_cast<const uint32_t *>(x + r * stride + c));
-                s[0] = __fadd_rn(s[0], __uint_as_float(v << 16));
-                s[1] = __fadd_rn(s[1], __uint_as_float(v & 0xFFFF0000u));
-            } else {
-                s[0] = __fadd_rn(s[0], bf16_bits_to_float(__ldg(x + r * stride + c)));
-            }
+        for (uint64_t r = rank * 32 + warp; r < rows; r += 256) {
+            const R v = load_unit<uint16_t, Q>(x + r * stride + c);
+#pragma unroll
+            for (int j = 0; j < Q; ++j) s[j] = __fadd_rn(s[j], v.get(j));
         }
     }
 #pragma unroll
-    for (int j = 0; j < Q; ++j) sums[warp][lane * Q + j] = s[j];
+    for (int j = 0; j < Q; ++j) sums[warp][j * 32 + lane] = s[j];
     __syncthreads();
     if (threadIdx.x < 32 * Q) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) v = __fadd_rn(v, sums[w][threadIdx.x]);
+        for (int w = 0; w < 32; ++w) v = __fadd_rn(v, sums[w][threadIdx.x]);
         total[threadIdx.x] = v;
     }
     cluster_sync();
-    const uint64_t mine = static_cast<uint64_t>(blockIdx.x / 8) * 32 * Q + threadIdx.x;
+    const uint64_t mine = first + (threadIdx.x & 31) * Q + threadIdx.x / 32;
     if (rank == 0 && threadIdx.x < 32 * Q && mine < cols) {
         float v = 0.0f;
 #pragma unroll
@@ -545,10 +545,10 @@ __global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(256)
 }
 
 cudaError_t launch_column_sums(const ProductParams &p, cudaStream_t stream) {
-    const bool pairs = p.N % 2 == 0 && p.dy_stride % 2 == 0 && (reinterpret_cast<uintptr_t>(p.dy) & 3) == 0;
-    const int cols = pairs ? 64 : 32;
-    const auto kernel = pairs ? column_sums<2> : column_sums<1>;
-    kernel<<<static_cast<unsigned>(8 * ((p.N + cols - 1) / cols)), 256, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N, p.dbias,
+    const bool eights = p.N % 8 == 0 && tma_fits(p.dy, p.dy_stride, 2);
+    const int cols = eights ? 256 : 32;
+    const auto kernel = eights ? column_sums<8> : column_sums<1>;
+    kernel<<<static_cast<unsigned>(8 * ((p.N + cols - 1) / cols)), 1024, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N, p.dbias,
                                                                                     p.accumulate);
     return cudaGetLastError();
 }
@@ -556,6 +556,8 @@ cudaError_t launch_column_sums(const ProductParams &p, cudaStream_t stream) {
 // Rows of 16-bit elements copied to rows that TMA can read.
 __global__ void copy_rows(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t dim, uint16_t *out,
                           uint64_t out_stride) {
+    let_next_start();
+    after_previous();
     for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x)
         for (uint64_t j = threadIdx.x; j < dim; j += blockDim.x) out[r * out_stride + j] = x[r * stride + j];
 }
@@ -595,8 +597,8 @@ cudaError_t readable_dy(const ProductParams &p, void *room, Operand &op, cudaStr
     if (tma_fits(p.dy, p.dy_stride, 2)) return cudaSuccess;
     op = {room, p.T, p.N, padded(p.N)};
     const int grid = persistent_grid(reinterpret_cast<const void *>(&copy_rows), 256, p.T);
-    copy_rows<<<grid, 256, 0, stream>>>(p.dy, p.dy_stride, p.T, p.N, static_cast<uint16_t *>(room), padded(p.N));
-    return cudaGetLastError();
+    return launch_chained(copy_rows, grid, 256, 0, stream, p.dy, p.dy_stride, p.T, p.N, static_cast<uint16_t *>(room),
+                          padded(p.N));
 }
 
 GemmParams outputs(const ProductParams &p, uint64_t M, uint64_t N, uint64_t L) {
@@ -617,7 +619,7 @@ GemmParams outputs(const ProductParams &p, uint64_t M, uint64_t N, uint64_t L) {
 cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
     const uint64_t work = p.M * ((p.N + 3) / 4);
     const int grid = persistent_grid(reinterpret_cast<const void *>(&join), 256, (work + 255) / 256);
-    join<<<grid, 256, 0, stream>>>(p);
+    join<<<grid, 256, 0, stream>>>(p);  // chained, it measured 1 us slower
     return cudaGetLastError();
 }
 

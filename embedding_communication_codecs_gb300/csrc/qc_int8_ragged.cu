@@ -7,6 +7,7 @@
 // that reach outside the matrix are not read: those units load single elements.
 #include <algorithm>
 
+#include "qc_chain.cuh"
 #include "qc_int8_rows.cuh"
 #include "qc_internal.h"
 
@@ -151,6 +152,7 @@ __device__ __forceinline__ RawCodes<U> load_codes_any(const int8_t *row, int e, 
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kRowThreads) ragged_decode(const RowCodesParams P, uint32_t lanes) {
+    let_next_start();
     constexpr int U = 16 / sizeof(T);
     const Team team(lanes);
     const int dim = static_cast<int>(P.dim);

@@ -11,6 +11,7 @@
 // instruction; rows that start anywhere are qc_int8_ragged.cu's.
 #include <algorithm>
 
+#include "qc_chain.cuh"
 #include "qc_int8_rows.cuh"
 #include "qc_internal.h"
 #include "qc_pipeline.cuh"
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(kRowThreads, BLOCKS) rows_encode(const RowCode
 
 template <typename T, int U, int V>
 __global__ void __launch_bounds__(kRowThreads) rows_decode(const RowCodesParams P, uint32_t lanes) {
+    let_next_start();
     const Team team(lanes);
     const uint32_t units = P.dim / U;
     for (uint64_t row = team.first; row < P.rows; row += team.stride) {

@@ -456,6 +456,82 @@ def test_swiglu_gradient_against_differences(q):
     check(d[:, dim:], du, size * (plain.U * 64 + 1e-9))
 
 
+# ------------------------------------- the kernels that only larger sizes reach
+
+def by_torch(codes, scale):
+    return codes.double() * scale.double()[:, None]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,dim", [(2000, 4096), (1001, 2056), (500, 8200), (460, 16384), (60000, 64), (3700, 1000),
+                                      (1300, 4099), (70000, 71), (500, 9001)])
+def test_many_rows(q, rows, dim, dtype):
+    """Row counts that fill the device: the streaming gated activation and the ragged
+    rows' one-warp teams, against torch in 64 bits; some rows are zero, infinite or NaN."""
+    gen = torch.Generator(device="cuda").manual_seed(rows * 31 + dim)
+    x = 2 * torch.randn((rows, 2 * dim), generator=gen, device="cuda")
+    x[3] = 0
+    x[7, dim + 1] = float("nan")
+    x[rows - 1, 5] = float("inf")
+    x = x.to(dtype)
+    hc, hs, sc, ss = q.swiglu_encode(x)
+    g, u = x[:, :dim].contiguous(), x[:, dim:].contiguous()
+    for half, part in ((0, g), (1, u)):        # gate and up are coded as rows of their own
+        codes, scale = q.rowwise_int8(part)
+        assert torch.equal(sc[:, half * dim:(half + 1) * dim], codes)
+        assert torch.equal(ss[:, half].view(torch.int32), scale.view(torch.int32))
+        live = torch.isfinite(part).all(1)
+        a = part.double().abs().amax(1)
+        assert bool((torch.isnan(scale) == ~live).all())
+        s = scale.double()[live]
+        assert bool((torch.frexp(s)[0] == 0.5).logical_or(s == 0).all())
+        assert bool(((a[live] < 127.5 * s) & (a[live] >= 63.75 * s)).logical_or(s == 0).all())
+        err = (by_torch(codes, scale) - part.double()).abs()[live]
+        assert bool((err <= 0.5 * s[:, None]).all())
+    h = g.double() * torch.sigmoid(g.double()) * u.double()
+    live = torch.isfinite(h).all(1)
+    assert bool((torch.isnan(hs) == ~live).all())
+    err = (by_torch(hc, hs) - h).abs()[live]
+    assert bool((err <= 0.5 * hs.double()[live][:, None] + h.abs()[live] * H_REL + 1e-44).all())
+    assert q.qc_take_device_errors() == 0
+
+
+@pytest.mark.parametrize("T,N,K", [(20, 20000, 512), (100, 33000, 256), (300, 10000, 1024), (2100, 2300, 600),
+                                   (4, 6000, 4096), (8, 4864, 320), (600, 512, 12000), (130, 128, 16384)])
+def test_larger_products(q, T, N, K):
+    """Several units of work to a block, split contractions with a short last range,
+    every token tile: integers below 2^24 in all sums, so one right answer."""
+    gen = torch.Generator(device="cuda").manual_seed(T + N + K)
+
+    def ints(lim, *shape):
+        return torch.randint(-lim, lim + 1, shape, generator=gen, device="cuda")
+    lim = 127 if K * 127 * 127 < 2 ** 24 else 32 if K * 32 * 32 < 2 ** 24 else 31
+    x, w = ints(lim, T, K).to(torch.int8), ints(lim, N, K).to(torch.int8)
+    one_t, one_n = torch.ones(T, device="cuda"), torch.ones(N, device="cuda")
+    y = q.int8_matmul(x, one_t, w, one_n, dtype=F32)
+    assert torch.equal(y.double(), x.double() @ w.double().t())
+    dy = ints(2, T, N).to(BF16)
+    assert torch.equal(q.int8_input_grad(dy, w, one_n, dtype=F32).double(), dy.double() @ w.double())
+    dw, db = q.int8_weight_grad(dy, x, one_t, with_bias=True)
+    assert torch.equal(dw.double(), dy.double().t() @ x.double())
+    assert torch.equal(db.double(), dy.double().sum(0))
+    assert q.qc_take_device_errors() == 0
+
+
+def test_long_sums_keep_their_precision(q):
+    """A weight gradient over 16384 tokens: cut into parts, the sum's error stays that of
+    a part of 2048 terms (each addition off by at most a unit in the last place of the
+    running sum, which for terms of random sign is the root of their number times one)."""
+    T, N, K = 16384, 256, 256
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    xc, xs = q.rowwise_int8(torch.randn((T, K), generator=gen, device="cuda"))
+    dy = torch.randn((T, N), generator=gen, device="cuda").to(BF16)
+    dw, _ = q.int8_weight_grad(dy, xc, xs)
+    want = dy.double().t() @ by_torch(xc, xs)
+    # 2048 / 16 additions of at most 2^-23 of a sum no larger than the result, plus the joins
+    assert float((dw.double() - want).norm() / want.norm()) <= (2048 / 16 + 8 + 16) * 2.0 ** -23
+
+
 # ------------------------------------------------------------ how it is run
 
 def test_other_stream_and_repeat(q):
