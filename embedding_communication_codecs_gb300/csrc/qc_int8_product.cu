@@ -20,7 +20,6 @@
 #include <cuda.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "qc_chain.cuh"
 #include "qc_int8_rows.cuh"
@@ -553,15 +552,6 @@ cudaError_t launch_column_sums(const ProductParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// Rows of 16-bit elements copied to rows that TMA can read.
-__global__ void copy_rows(const uint16_t *x, uint64_t stride, uint64_t rows, uint64_t dim, uint16_t *out,
-                          uint64_t out_stride) {
-    let_next_start();
-    after_previous();
-    for (uint64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (uint64_t j = threadIdx.x; j < dim; j += blockDim.x) out[r * out_stride + j] = x[r * stride + j];
-}
-
 // Row length, in elements, of a widened matrix in the workspace: whole 128-byte rows.
 uint64_t padded(uint64_t dim) { return (dim + 63) / 64 * 64; }
 uint64_t widened_bytes(uint64_t rows, uint64_t dim) { return (rows * padded(dim) * 2 + 255) / 256 * 256; }
@@ -596,9 +586,8 @@ cudaError_t readable_dy(const ProductParams &p, void *room, Operand &op, cudaStr
     op = {p.dy, p.T, p.N, p.dy_stride};
     if (tma_fits(p.dy, p.dy_stride, 2)) return cudaSuccess;
     op = {room, p.T, p.N, padded(p.N)};
-    const int grid = persistent_grid(reinterpret_cast<const void *>(&copy_rows), 256, p.T);
-    return launch_chained(copy_rows, grid, 256, 0, stream, p.dy, p.dy_stride, p.T, p.N, static_cast<uint16_t *>(room),
-                          padded(p.N));
+    return launch_ragged_copy16(p.dy, p.dy_stride, p.T, static_cast<uint32_t>(p.N), static_cast<uint16_t *>(room), padded(p.N),
+                                stream);
 }
 
 GemmParams outputs(const ProductParams &p, uint64_t M, uint64_t N, uint64_t L) {
@@ -623,15 +612,20 @@ cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// Which kernel multiplies T tokens: the weights are read as codes by qc_int8_few.cu
-// up to kFewTokens and by qc_int8_wide.cu up to kWideTokens; beyond, the weights are
-// widened once and the tiles of this file take both operands from memory.
-constexpr uint64_t kFewTokens = 16, kWideTokens = 512;
+// Which kernel multiplies T tokens: the weights are read as codes by qc_int8_few.cu up
+// to kFewTokens and by qc_int8_wide.cu up to kWideTokens; beyond, both operands are
+// widened in memory and this file's tiles multiply them.  Weights of 4096 x 4096: 16
+// tokens take 7 us against the next kernel's 10, 256 take 21 us against 26, 512 27 against
+// 32, and 1024 33 against 63.  Codes that TMA cannot read where they lie are copied first
+// for qc_int8_wide.cu, which pays up to kWideCopied (11000 x 4097: 128 tokens 45 us
+// against 63, 512 tokens 96 against 85).
+constexpr uint64_t kFewTokens = 16, kWideTokens = 512, kWideCopied = 256;
 
 size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K) {
     if (T <= kFewTokens) return 0;
-    const size_t wide = T <= kWideTokens ? wide_tokens_workspace(T, N, K) : 0;
-    return std::max(wide, widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K));
+    if (T <= kWideCopied) return wide_tokens_workspace(T, N, K);
+    const size_t tiles = widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K);
+    return T <= kWideTokens ? std::max(tiles, wide_tokens_workspace(T, N, K)) : tiles;
 }
 size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
     return widened_bytes(N, K) + widened_bytes(T, N) + partial_bytes(T, K, N);
@@ -642,7 +636,7 @@ size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
     if (p.T <= kFewTokens) return launch_int8_few(p, stream);
-    if (p.T <= kWideTokens && wide_tokens_fit(p.x_codes, p.w_codes, p.K)) return launch_int8_wide(p, stream);
+    if (p.T <= kWideCopied || (p.T <= kWideTokens && wide_tokens_readable(p))) return launch_int8_wide(p, stream);
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     const Widen x{p.x_codes, nullptr, p.T, ws}, w{p.w_codes, nullptr, p.N, ws + widened_bytes(p.T, p.K)};
     const cudaError_t e = widen(p.K, x, w, stream);

@@ -242,6 +242,34 @@ __global__ void __launch_bounds__(kRowThreads, 4) ragged_swiglu_encode(const Swi
     }
 }
 
+// Rows of 16-bit elements, or of codes, copied to rows on 16-byte boundaries, as TMA
+// reads them.
+__global__ void __launch_bounds__(kRowThreads) ragged_copy16(const uint16_t *x, uint64_t stride, uint64_t rows, uint32_t dim,
+                                                             uint16_t *out, uint64_t out_stride, uint32_t lanes) {
+    let_next_start();
+    after_previous();
+    const Team team(lanes);
+    const uint16_t *end = x + (rows - 1) * stride + dim;
+    for (uint64_t r = team.first; r < rows; r += team.stride)
+#pragma unroll 4
+        for (uint32_t e = 8 * team.lane; e < dim; e += 8 * lanes)
+            *reinterpret_cast<RawBf16<8> *>(out + r * out_stride + e) =
+                load8_any<false>(x + r * stride, static_cast<int>(e), static_cast<int>(dim), x, end);
+}
+
+__global__ void __launch_bounds__(kRowThreads) ragged_copy8(const int8_t *codes, uint64_t rows, uint32_t dim, int8_t *out,
+                                                            uint64_t out_stride, uint32_t lanes) {
+    let_next_start();
+    const Team team(lanes);
+    const int8_t *end = codes + rows * dim;
+    for (uint64_t r = team.first; r < rows; r += team.stride)
+#pragma unroll 4
+        for (uint32_t e = 16 * team.lane; e < dim; e += 16 * lanes) {
+            const RawCodes<16> c = load_codes_any<16>(codes + r * dim, static_cast<int>(e), static_cast<int>(dim), codes, end);
+            *reinterpret_cast<uint4 *>(out + r * out_stride + e) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+        }
+}
+
 // Whether codes on 8 bytes are elements of `esize` bytes on 8 of them, in every row.
 bool in_step(const void *x, uint64_t x_stride, size_t esize, const void *codes, uint64_t dim) {
     return x_stride == dim && reinterpret_cast<uintptr_t>(x) % (8 * esize) == reinterpret_cast<uintptr_t>(codes) % 8 * esize;
@@ -274,6 +302,23 @@ cudaError_t decode(const RowCodesParams &p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_ragged_copy16(const uint16_t *x, uint64_t stride, uint64_t rows, uint32_t dim, uint16_t *out,
+                                 uint64_t out_stride, cudaStream_t stream) {
+    const uint32_t lanes = lanes_for((dim + 7) / 8, 4, kRowThreads);
+    const uint64_t teams = kRowThreads / lanes;
+    const int grid = persistent_grid(reinterpret_cast<const void *>(&ragged_copy16), kRowThreads, (rows + teams - 1) / teams);
+    return launch_chained(ragged_copy16, grid, kRowThreads, 0, stream, x, stride, rows, dim, out, out_stride, lanes);
+}
+
+cudaError_t launch_ragged_copy8(const int8_t *codes, uint64_t rows, uint32_t dim, int8_t *out, uint64_t out_stride,
+                                cudaStream_t stream) {
+    const uint32_t lanes = lanes_for((dim + 15) / 16, 4, kRowThreads);
+    const uint64_t teams = kRowThreads / lanes;
+    const int grid = persistent_grid(reinterpret_cast<const void *>(&ragged_copy8), kRowThreads, (rows + teams - 1) / teams);
+    ragged_copy8<<<grid, kRowThreads, 0, stream>>>(codes, rows, dim, out, out_stride, lanes);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_ragged_encode(const RowCodesParams &p, int bf16, cudaStream_t stream) {
     if (in_step(p.x, p.x_stride, bf16 ? 2 : 4, p.codes, p.dim))

@@ -307,9 +307,10 @@ WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     return best;
 }
 
-// Rows of K codes as boxes of 128 codes under the 128-byte swizzle; zeros outside.
-bool map_codes(CUtensorMap *map, const int8_t *p, uint64_t rows, uint64_t K, uint32_t box_rows) {
-    const cuuint64_t dims[2] = {K, rows}, strides[1] = {K};
+// Rows of K codes, `pitch` bytes apart, as boxes of 128 codes under the 128-byte
+// swizzle; zeros outside.
+bool map_codes(CUtensorMap *map, const int8_t *p, uint64_t rows, uint64_t K, uint64_t pitch, uint32_t box_rows) {
+    const cuuint64_t dims[2] = {K, rows}, strides[1] = {pitch};
     const cuuint32_t box[2] = {kStepK, box_rows}, unit[2] = {1, 1};
     EncodeTiled fn = encode_tiled();
     return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(p), dims, strides, box, unit,
@@ -317,12 +318,21 @@ bool map_codes(CUtensorMap *map, const int8_t *p, uint64_t rows, uint64_t K, uin
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Codes as TMA reads them: rows on 16-byte boundaries.
+struct Codes {
+    const int8_t *p;
+    uint64_t pitch;
+};
+bool readable(const int8_t *p, uint64_t K) { return K % 16 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+uint64_t pitch16(uint64_t K) { return (K + 15) / 16 * 16; }
+uint64_t copied_bytes(uint64_t rows, uint64_t K) { return (rows * pitch16(K) + 255) / 256 * 256; }
+
 template <int BT>
-cudaError_t launch_wide(const ProductParams &p, const WideParams &w, cudaStream_t stream) {
+cudaError_t launch_wide(const ProductParams &p, const Codes &wc, const Codes &xc, const WideParams &w, cudaStream_t stream) {
     using C = Wide<BT>;
     const auto kernel = wide_tokens<BT>;
     CUtensorMap mw, mx;
-    if (!map_codes(&mw, p.w_codes, p.N, p.K, kRows) || !map_codes(&mx, p.x_codes, p.T, p.K, BT)) return cudaErrorInvalidValue;
+    if (!map_codes(&mw, wc.p, p.N, p.K, wc.pitch, kRows) || !map_codes(&mx, xc.p, p.T, p.K, xc.pitch, BT)) return cudaErrorInvalidValue;
     const cudaError_t e = prepare_dynamic_smem(reinterpret_cast<const void *>(kernel), C::kSmem);
     if (e != cudaSuccess) return e;
     const uint64_t units = ((p.T + BT - 1) / BT) * ((p.N + kRows - 1) / kRows) * w.splits, most = sm_count();
@@ -332,13 +342,14 @@ cudaError_t launch_wide(const ProductParams &p, const WideParams &w, cudaStream_
 
 }  // namespace
 
-bool wide_tokens_fit(const void *x_codes, const void *w_codes, uint64_t K) {
-    return K % 16 == 0 && ((reinterpret_cast<uintptr_t>(x_codes) | reinterpret_cast<uintptr_t>(w_codes)) & 15) == 0;
-}
+bool wide_tokens_readable(const ProductParams &p) { return readable(p.w_codes, p.K) && readable(p.x_codes, p.K); }
 
+// Room for the sums of a split contraction and, for codes that TMA cannot read where
+// they lie, for copies of both matrices.  The bases' alignment is not known here, so
+// the copies have room whatever K is.
 size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K) {
     const WidePlan plan = wide_plan(T, N, K);
-    return plan.splits > 1 ? plan.splits * ceil32(T) * ceil32(N) * 4 : 0;
+    return (plan.splits > 1 ? plan.splits * ceil32(T) * ceil32(N) * 4 : 0) + copied_bytes(N, K) + copied_bytes(T, K);
 }
 
 cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream) {
@@ -357,9 +368,20 @@ cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream) {
     w.w_scale = p.w_scale;
     w.bias = p.bias;
     w.status = p.status;
-    const cudaError_t e = plan.bt == 32   ? launch_wide<32>(p, w, stream)
-                          : plan.bt == 64 ? launch_wide<64>(p, w, stream)
-                                          : launch_wide<128>(p, w, stream);
+    Codes wc{p.w_codes, p.K}, xc{p.x_codes, p.K};
+    cudaError_t e = cudaSuccess;
+    if (!wide_tokens_readable(p)) {
+        int8_t *room = static_cast<int8_t *>(p.workspace) + (plan.splits > 1 ? plan.splits * ceil32(p.T) * ceil32(p.N) * 4 : 0);
+        wc = {room, pitch16(p.K)};
+        xc = {room + copied_bytes(p.N, p.K), pitch16(p.K)};
+        e = launch_ragged_copy8(p.w_codes, p.N, static_cast<uint32_t>(p.K), room, wc.pitch, stream);
+        if (e == cudaSuccess)
+            e = launch_ragged_copy8(p.x_codes, p.T, static_cast<uint32_t>(p.K), room + copied_bytes(p.N, p.K), xc.pitch, stream);
+        if (e != cudaSuccess) return e;
+    }
+    e = plan.bt == 32   ? launch_wide<32>(p, wc, xc, w, stream)
+        : plan.bt == 64 ? launch_wide<64>(p, wc, xc, w, stream)
+                        : launch_wide<128>(p, wc, xc, w, stream);
     if (e != cudaSuccess || w.splits == 1) return e;
     return launch_join({w.partial, w.splits, p.T, p.N, p.out, p.out_stride, p.out_bf16, 0, p.x_scale, p.w_scale, p.bias}, stream);
 }

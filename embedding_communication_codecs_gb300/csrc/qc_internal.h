@@ -337,6 +337,12 @@ cudaError_t launch_swiglu_backward(const SwigluParams &p, int bf16, cudaStream_t
 // The same for rows that start anywhere (qc_int8_ragged.cu).
 cudaError_t launch_ragged_encode(const RowCodesParams &p, int bf16, cudaStream_t stream);
 cudaError_t launch_ragged_decode(const RowCodesParams &p, int bf16, cudaStream_t stream);
+// Rows of 16-bit elements or of codes copied to rows on 16-byte boundaries (out_stride
+// covers whole 16-byte pieces; what lies past dim in the last one is unspecified).
+cudaError_t launch_ragged_copy16(const uint16_t *x, uint64_t stride, uint64_t rows, uint32_t dim, uint16_t *out,
+                                 uint64_t out_stride, cudaStream_t stream);
+cudaError_t launch_ragged_copy8(const int8_t *codes, uint64_t rows, uint32_t dim, int8_t *out, uint64_t out_stride,
+                                cudaStream_t stream);
 cudaError_t launch_ragged_swiglu_encode(const SwigluParams &p, int bf16, cudaStream_t stream);
 
 // One product of the layer: out[M, N] = sum over L of the operands named per launcher.
@@ -372,9 +378,9 @@ struct JoinParams {
 inline uint64_t ceil32(uint64_t v) { return (v + 31) / 32 * 32; }
 cudaError_t launch_join(const JoinParams &p, cudaStream_t stream);
 
-// The product for a batch of tokens, the weights read as codes (qc_int8_wide.cu);
-// wide_tokens_fit(): TMA can read the rows of both.
-bool wide_tokens_fit(const void *x_codes, const void *w_codes, uint64_t K);
+// The product for a batch of tokens, the weights read as codes (qc_int8_wide.cu).
+// wide_tokens_readable(): TMA reads the codes where they lie.
+bool wide_tokens_readable(const ProductParams &p);
 size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K);
 cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream);
 
