@@ -43,11 +43,17 @@ struct Wide {
     static constexpr int kBytesW = kRows * kStepK, kBytesX = BT * kStepK;  // codes of a step
     static constexpr int kCodes = kBytesW + kBytesX;
     static constexpr int kBytesF = BT * kStepK * 2;                       // widened tokens of a step
-    static constexpr int kRing = BT == 128 ? 3 : 7;
-    static constexpr int kStages = BT == 32 ? 8 : BT == 64 ? 4 : 3;
+    static constexpr int kRing = BT == 32 ? 7 : BT == 64 ? 4 : 3;
+    static constexpr int kStages = BT == 32 ? 8 : BT == 64 ? 6 : 3;
     static constexpr int kFirstA = kTmemCols - kRing * kACols;
     static constexpr int kSmem = kStages * kCodes + kRing * kBytesF + 1024;
     static_assert(kFirstA >= BT, "the sums and the ring share tensor memory");
+    // A barrier's wait tells a phase from the one before it, not from the one before
+    // that.  A group at step i has passed step i - kGroups, whose slot was freed by step
+    // i - kGroups - kRing, and the instructions go in order: so the slot's last phase but one
+    // is over (i - 2 kRing <= i - kGroups - kRing), and once the slot of step i is free, step
+    // i - kRing is done and with it the stage's last user (i - kStages <= i - kRing).
+    static_assert(kRing >= kGroups && kStages >= kRing, "no wait may pass on an older phase");
 };
 
 struct WideParams {
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t k = 0; k < w.steps; ++k, ++it) {
                 if (it % kGroups != group) continue;
                 const uint32_t s = it % S, r = it % R;
-                ok = mbar_wait(&full[s], (it / S) & 1);
+                ok = mbar_wait(&freed[r], ((it / R) & 1) ^ 1) && mbar_wait(&full[s], (it / S) & 1);
                 const uint8_t *from = codes + s * C::kCodes;
                 uint4 c[8], x[BT / 16];
 #pragma unroll
@@ -193,7 +199,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int t = i * 16 + (row >> 3), p = row & 7;
                     x[i] = *reinterpret_cast<const uint4 *>(from + C::kBytesW + t * 128 + ((p ^ (t & 7)) << 4));
                 }
-                ok = ok && mbar_wait(&freed[r], ((it / R) & 1) ^ 1);
                 if (__any_sync(kFull, !ok)) {
                     ok = false;
                     break;
