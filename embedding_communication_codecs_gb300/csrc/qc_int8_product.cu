@@ -617,13 +617,19 @@ cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
 // widened in memory and this file's tiles multiply them.  Weights of 4096 x 4096: 16
 // tokens take 7 us against the next kernel's 10, 256 take 21 us against 26, 512 27 against
 // 32, and 1024 33 against 63.  Codes that TMA cannot read where they lie are copied first
-// for qc_int8_wide.cu, which pays up to kWideCopied (11000 x 4097: 128 tokens 45 us
-// against 63, 512 tokens 96 against 85).
-constexpr uint64_t kFewTokens = 16, kWideTokens = 512, kWideCopied = 256;
+// for qc_int8_wide.cu, which always pays up to kWideCopiedFew tokens (1000 x 1001: 64 tokens
+// 10.3 us against 11.7) and for large weights up to kWideCopied: 4096 x 4097, 256 tokens
+// 28.8 us against 33.3, but 2000 x 2001 16.3 against 15.1.
+constexpr uint64_t kFewTokens = 16, kWideTokens = 512, kWideCopiedFew = 64, kWideCopied = 256;
+constexpr uint64_t kWideCopiedWeights = 1u << 23;
+
+bool wide_with_copies(uint64_t T, uint64_t N, uint64_t K) {
+    return T <= kWideCopiedFew || (T <= kWideCopied && N * K >= kWideCopiedWeights);
+}
 
 size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K) {
     if (T <= kFewTokens) return 0;
-    if (T <= kWideCopied) return wide_tokens_workspace(T, N, K);
+    if (wide_with_copies(T, N, K)) return wide_tokens_workspace(T, N, K);
     const size_t tiles = widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K);
     return T <= kWideTokens ? std::max(tiles, wide_tokens_workspace(T, N, K)) : tiles;
 }
@@ -636,7 +642,7 @@ size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
     if (p.T <= kFewTokens) return launch_int8_few(p, stream);
-    if (p.T <= kWideCopied || (p.T <= kWideTokens && wide_tokens_readable(p))) return launch_int8_wide(p, stream);
+    if (wide_with_copies(p.T, p.N, p.K) || (p.T <= kWideTokens && wide_tokens_readable(p))) return launch_int8_wide(p, stream);
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     const Widen x{p.x_codes, nullptr, p.T, ws}, w{p.w_codes, nullptr, p.N, ws + widened_bytes(p.T, p.K)};
     const cudaError_t e = widen(p.K, x, w, stream);

@@ -257,17 +257,22 @@ __global__ void __launch_bounds__(kRowThreads) ragged_copy16(const uint16_t *x, 
                 load8_any<false>(x + r * stride, static_cast<int>(e), static_cast<int>(dim), x, end);
 }
 
-__global__ void __launch_bounds__(kRowThreads) ragged_copy8(const int8_t *codes, uint64_t rows, uint32_t dim, int8_t *out,
-                                                            uint64_t out_stride, uint32_t lanes) {
-    let_next_start();
+// Two matrices of codes of one row length in one launch.
+__global__ void __launch_bounds__(kRowThreads) ragged_copy8(const int8_t *a, uint64_t rows_a, int8_t *to_a, const int8_t *b,
+                                                            uint64_t rows_b, int8_t *to_b, uint32_t dim, uint64_t out_stride,
+                                                            uint32_t lanes) {
     const Team team(lanes);
-    const int8_t *end = codes + rows * dim;
-    for (uint64_t r = team.first; r < rows; r += team.stride)
+    for (uint64_t row = team.first; row < rows_a + rows_b; row += team.stride) {
+        const bool second = row >= rows_a;
+        const uint64_t r = second ? row - rows_a : row;
+        const int8_t *codes = second ? b : a, *end = codes + (second ? rows_b : rows_a) * dim;
+        int8_t *out = (second ? to_b : to_a) + r * out_stride;
 #pragma unroll 4
         for (uint32_t e = 16 * team.lane; e < dim; e += 16 * lanes) {
             const RawCodes<16> c = load_codes_any<16>(codes + r * dim, static_cast<int>(e), static_cast<int>(dim), codes, end);
-            *reinterpret_cast<uint4 *>(out + r * out_stride + e) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
+            *reinterpret_cast<uint4 *>(out + e) = make_uint4(c.w[0], c.w[1], c.w[2], c.w[3]);
         }
+    }
 }
 
 // Whether codes on 8 bytes are elements of `esize` bytes on 8 of them, in every row.
@@ -311,12 +316,12 @@ cudaError_t launch_ragged_copy16(const uint16_t *x, uint64_t stride, uint64_t ro
     return launch_chained(ragged_copy16, grid, kRowThreads, 0, stream, x, stride, rows, dim, out, out_stride, lanes);
 }
 
-cudaError_t launch_ragged_copy8(const int8_t *codes, uint64_t rows, uint32_t dim, int8_t *out, uint64_t out_stride,
-                                cudaStream_t stream) {
+cudaError_t launch_ragged_copy8(const int8_t *a, uint64_t rows_a, int8_t *to_a, const int8_t *b, uint64_t rows_b, int8_t *to_b,
+                                uint32_t dim, uint64_t out_stride, cudaStream_t stream) {
     const uint32_t lanes = lanes_for((dim + 15) / 16, 4, kRowThreads);
     const uint64_t teams = kRowThreads / lanes;
-    const int grid = persistent_grid(reinterpret_cast<const void *>(&ragged_copy8), kRowThreads, (rows + teams - 1) / teams);
-    ragged_copy8<<<grid, kRowThreads, 0, stream>>>(codes, rows, dim, out, out_stride, lanes);
+    const int grid = persistent_grid(reinterpret_cast<const void *>(&ragged_copy8), kRowThreads, (rows_a + rows_b + teams - 1) / teams);
+    ragged_copy8<<<grid, kRowThreads, 0, stream>>>(a, rows_a, to_a, b, rows_b, to_b, dim, out_stride, lanes);
     return cudaGetLastError();
 }
 

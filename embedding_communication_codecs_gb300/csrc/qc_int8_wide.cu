@@ -14,8 +14,8 @@
 // instructions, and warps 4 to 15 widen and, at the end, store: three groups of four
 // (a warp reaches 32 lanes of tensor memory) take every third step, so that the
 // latency of a step, several hundred cycles of waits and conversions, is paid three
-// at a time.  The ring of kRing widened steps is as long as tensor memory (64 columns a step
-// next to BT columns of sums) and shared memory allow.
+// at a time.  Tensor memory (64 columns a step next to BT columns of sums) and shared
+// memory bound the ring of kRing widened steps, and the waits its ratio to the stages.
 // The lanes of a storing warp hold neighbouring outputs of one token, so its stores
 // are whole lines wherever y's rows start.
 #include <cuda.h>
@@ -379,9 +379,8 @@ cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream) {
         int8_t *room = static_cast<int8_t *>(p.workspace) + (plan.splits > 1 ? plan.splits * ceil32(p.T) * ceil32(p.N) * 4 : 0);
         wc = {room, pitch16(p.K)};
         xc = {room + copied_bytes(p.N, p.K), pitch16(p.K)};
-        e = launch_ragged_copy8(p.w_codes, p.N, static_cast<uint32_t>(p.K), room, wc.pitch, stream);
-        if (e == cudaSuccess)
-            e = launch_ragged_copy8(p.x_codes, p.T, static_cast<uint32_t>(p.K), room + copied_bytes(p.N, p.K), xc.pitch, stream);
+        e = launch_ragged_copy8(p.w_codes, p.N, room, p.x_codes, p.T, room + copied_bytes(p.N, p.K), static_cast<uint32_t>(p.K),
+                                wc.pitch, stream);
         if (e != cudaSuccess) return e;
     }
     e = plan.bt == 32   ? launch_wide<32>(p, wc, xc, w, stream)

@@ -337,12 +337,12 @@ cudaError_t launch_swiglu_backward(const SwigluParams &p, int bf16, cudaStream_t
 // The same for rows that start anywhere (qc_int8_ragged.cu).
 cudaError_t launch_ragged_encode(const RowCodesParams &p, int bf16, cudaStream_t stream);
 cudaError_t launch_ragged_decode(const RowCodesParams &p, int bf16, cudaStream_t stream);
-// Rows of 16-bit elements or of codes copied to rows on 16-byte boundaries (out_stride
+// Rows of 16-bit elements, or of two matrices of codes, copied to rows on 16-byte boundaries (out_stride
 // covers whole 16-byte pieces; what lies past dim in the last one is unspecified).
 cudaError_t launch_ragged_copy16(const uint16_t *x, uint64_t stride, uint64_t rows, uint32_t dim, uint16_t *out,
                                  uint64_t out_stride, cudaStream_t stream);
-cudaError_t launch_ragged_copy8(const int8_t *codes, uint64_t rows, uint32_t dim, int8_t *out, uint64_t out_stride,
-                                cudaStream_t stream);
+cudaError_t launch_ragged_copy8(const int8_t *a, uint64_t rows_a, int8_t *to_a, const int8_t *b, uint64_t rows_b, int8_t *to_b,
+                                uint32_t dim, uint64_t out_stride, cudaStream_t stream);
 cudaError_t launch_ragged_swiglu_encode(const SwigluParams &p, int bf16, cudaStream_t stream);
 
 // One product of the layer: out[M, N] = sum over L of the operands named per launcher.
