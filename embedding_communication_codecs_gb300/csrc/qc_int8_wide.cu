@@ -43,8 +43,8 @@ struct Wide {
     static constexpr int kBytesW = kRows * kStepK, kBytesX = BT * kStepK;  // codes of a step
     static constexpr int kCodes = kBytesW + kBytesX;
     static constexpr int kBytesF = BT * kStepK * 2;                       // widened tokens of a step
-    static constexpr int kRing = BT == 32 ? 7 : BT == 64 ? 4 : 3;
-    static constexpr int kStages = BT == 32 ? 8 : BT == 64 ? 6 : 3;
+    static constexpr int kRing = BT == 32 ? 7 : BT == 48 ? 5 : BT == 64 ? 4 : BT == 96 ? 4 : 3;
+    static constexpr int kStages = BT == 32 ? 8 : BT == 48 ? 7 : BT == 64 ? 6 : BT == 96 ? 4 : 3;
     static constexpr int kFirstA = kTmemCols - kRing * kACols;
     static constexpr int kSmem = kStages * kCodes + kRing * kBytesF + 1024;
     static_assert(kFirstA >= BT, "the sums and the ring share tensor memory");
@@ -182,9 +182,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = n < P.N;
             // what the stores will need, asked for before the sums are there
             const float ws = live ? __ldg(P.w_scale + n) : 0.0f, bias = live && P.bias ? __ldg(P.bias + n) : 0.0f;
-            float xs[BT / 32];
+            float xs[(BT + 31) / 32];
 #pragma unroll
-            for (int i = 0; i < BT / 32; ++i) xs[i] = 32 * i + lane < left ? __ldg(P.x_scale + t0 + 32 * i + lane) : 0.0f;
+            for (int i = 0; i < (BT + 31) / 32; ++i) xs[i] = 32 * i + lane < left ? __ldg(P.x_scale + t0 + 32 * i + lane) : 0.0f;
             for (uint32_t k = 0; k < w.steps; ++k, ++it) {
                 if (it % kGroups != group) continue;
                 const uint32_t s = it % S, r = it % R;
@@ -294,7 +294,8 @@ struct WidePlan {
 // launch and its sums written and read.
 WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     constexpr uint64_t kBlocks = 152;
-    const int bt = T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    const uint64_t most = (T + 127) / 128;
+    const int bt = T <= 32 * most ? 32 : T <= 48 * most ? 48 : T <= 64 * most ? 64 : T <= 96 * most ? 96 : 128;
     const uint64_t steps = (K + kStepK - 1) / kStepK;
     const uint64_t tiles = ((T + bt - 1) / bt) * ((N + kRows - 1) / kRows);
     WidePlan best{bt, 1, static_cast<uint32_t>(steps)};
@@ -302,7 +303,7 @@ WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     for (uint64_t s = 1; s <= 16 && (s == 1 || steps / s >= 2); ++s) {
         const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
         const uint64_t waves = (tiles * splits + kBlocks - 1) / kBlocks;
-        double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bt == 128 ? 1000 : 700) + 5000);
+        double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bt == 128 ? 1000 : bt == 96 ? 850 : 700) + 5000);
         if (splits > 1) cost += 6000 + static_cast<double>(splits) * T * N * 8 / 5000;
         if (cost < best_cost) {
             best_cost = cost;
@@ -384,6 +385,8 @@ cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     e = plan.bt == 32   ? launch_wide<32>(p, wc, xc, w, stream)
+        : plan.bt == 48 ? launch_wide<48>(p, wc, xc, w, stream)
+        : plan.bt == 96 ? launch_wide<96>(p, wc, xc, w, stream)
         : plan.bt == 64 ? launch_wide<64>(p, wc, xc, w, stream)
                         : launch_wide<128>(p, wc, xc, w, stream);
     if (e != cudaSuccess || w.splits == 1) return e;

@@ -19,8 +19,9 @@ def constants():
     groups = int(re.search(r"kGroups = (\d+)", text).group(1))
 
     def of(name):
-        m = re.search(name + r" = BT == 32 \? (\d+) : BT == 64 \? (\d+) : (\d+);", text)
-        return dict(zip((32, 64, 128), map(int, m.groups())))
+        text_of = re.search(name + r" = ((?:BT == \d+ \? \d+ : )+)(\d+);", text)
+        lengths = {int(t): int(n) for t, n in re.findall(r"BT == (\d+) \? (\d+)", text_of.group(1))}
+        return {**lengths, 128: int(text_of.group(2))}
     return groups, of("kRing"), of("kStages")
 
 
@@ -70,7 +71,7 @@ def run(stages, ring, groups, steps, seed):
             done += 1
 
 
-@pytest.mark.parametrize("tokens", [32, 64, 128])
+@pytest.mark.parametrize("tokens", [32, 48, 64, 96, 128])
 def test_no_wait_passes_on_an_older_phase(tokens):
     groups, ring, stages = constants()
     for seed in range(300):
