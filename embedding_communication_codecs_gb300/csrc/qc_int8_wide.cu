@@ -288,27 +288,32 @@ struct WidePlan {
     uint32_t splits, split_steps;
 };
 
-// Token tiles of 32, 64 or 128, and the contraction cut so that the SMs have work: a
-// step takes a block about 700 cycles at its share of the memory's rate (1000 with the
-// short ring of 128 tokens); a unit starts and stores in about 5000; a join is a
-// launch and its sums written and read.
+// The token tile and the cuts of the contraction that cost least, in ns.  A step takes
+// longer the wider the tile, as shared memory carries the tokens four times (codes in and
+// out, f16 in and out); a unit starts and stores; a join is a launch and its sums written
+// and read.  The figures were fitted to 1450 timed plans (1024 x 1024 to 16384 x 4096, 24 to
+// 512 tokens): 5 % off on average, and the choice within 3 % of the best.  Small weights
+// want many narrow tiles (1024 x 1024, 128 tokens: 6.7 us in tiles of 32, 11.4 in one of 128),
+// large ones as few as there are (16384 x 4096: 27.9 us in one, 33.8 in two of 64).  The
+// contraction is cut only as far as one unit for each SM.
 WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     constexpr uint64_t kBlocks = 152;
-    const uint64_t most = (T + 127) / 128;
-    const int bt = T <= 32 * most ? 32 : T <= 48 * most ? 48 : T <= 64 * most ? 64 : T <= 96 * most ? 96 : 128;
     const uint64_t steps = (K + kStepK - 1) / kStepK;
-    const uint64_t tiles = ((T + bt - 1) / bt) * ((N + kRows - 1) / kRows);
-    WidePlan best{bt, 1, static_cast<uint32_t>(steps)};
+    WidePlan best{};
     double best_cost = 1e300;
-    for (uint64_t s = 1; s <= 16 && (s == 1 || steps / s >= 2); ++s) {
-        const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
-        const uint64_t waves = (tiles * splits + kBlocks - 1) / kBlocks;
-        double cost = static_cast<double>(waves) * (static_cast<double>(per) * (bt == 128 ? 1000 : bt == 96 ? 850 : 700) + 5000);
-        if (splits > 1) cost += 6000 + static_cast<double>(splits) * T * N * 8 / 5000;
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = {bt, static_cast<uint32_t>(splits), static_cast<uint32_t>(per)};
+    for (const int bt : {32, 48, 64, 96, 128}) {
+        const uint64_t tiles = ((T + bt - 1) / bt) * ((N + kRows - 1) / kRows);
+        for (uint64_t s = 1; s == 1 || (s <= 16 && steps / s >= 2 && tiles * s <= kBlocks); ++s) {
+            const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
+            const uint64_t waves = (tiles * splits + kBlocks - 1) / kBlocks;
+            double cost = static_cast<double>(waves) * (static_cast<double>(per) * (240 + 2.6 * bt) + 300 + 21.0 * bt);
+            if (splits > 1) cost += 1800 + 0.0017 * static_cast<double>(splits) * static_cast<double>(T) * static_cast<double>(N);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = {bt, static_cast<uint32_t>(splits), static_cast<uint32_t>(per)};
+            }
         }
+        if (static_cast<uint64_t>(bt) >= T) break;
     }
     return best;
 }
