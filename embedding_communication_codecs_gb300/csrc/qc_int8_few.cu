@@ -19,6 +19,9 @@ namespace {
 
 constexpr int kFewWarps = 8;
 constexpr int kChunk = 64;
+// The matrix instruction's running sum drops what is below its last place; a warp's sum
+// is cut into parts of 32 chunks = 2048 terms, added in fp32.
+constexpr int kPartChunks = 32;
 
 struct FewParams {
     const int8_t *x, *w;
@@ -137,44 +140,52 @@ __global__ void __launch_bounds__(32 * kFewWarps, BLOCKS) few_tokens(const FewPa
     constexpr int kOut = 16, kTok = 8 * NT, kPitch = kOut + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const uint64_t n0 = static_cast<uint64_t>(blockIdx.x) * kOut, t0 = static_cast<uint64_t>(blockIdx.y) * kTok;
-    float acc[NT][4] = {};
-    const uint64_t step = kFewWarps * kChunk;
-    for (uint64_t k0 = static_cast<uint64_t>(warp) * kChunk; k0 < P.K; k0 += AHEAD * step) {
-        typename PieceOf<ALIGNED>::type w[AHEAD][2], x[AHEAD][NT];
+    static_assert(kPartChunks % AHEAD == 0, "parts are whole rounds of loads");
+    constexpr uint32_t step = kFewWarps * kChunk;
+    const uint32_t K = static_cast<uint32_t>(P.K);
+    float *mine = sums + warp * kTok * kPitch;
+    for (uint32_t part = 0; part < K; part += kPartChunks * step) {
+        float acc[NT][4] = {};
+        const uint32_t end = min(K, part + kPartChunks * step);
+        for (uint32_t k0 = part + warp * kChunk; k0 < end; k0 += AHEAD * step) {
+            typename PieceOf<ALIGNED>::type w[AHEAD][2], x[AHEAD][NT];
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const uint64_t k = k0 + a * step + 16 * q;
-            w[a][0] = load16<ALIGNED>(P.w, n0 + g, k, P.N, P.K);
-            w[a][1] = load16<ALIGNED>(P.w, n0 + g + 8, k, P.N, P.K);
+            for (int a = 0; a < AHEAD; ++a) {
+                const uint64_t k = k0 + a * step + 16 * q;
+                w[a][0] = load16<ALIGNED>(P.w, n0 + g, k, P.N, P.K);
+                w[a][1] = load16<ALIGNED>(P.w, n0 + g + 8, k, P.N, P.K);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) x[a][j] = load16<ALIGNED>(P.x, t0 + 8 * j + g, k, P.T, P.K);
-        }
+                for (int j = 0; j < NT; ++j) x[a][j] = load16<ALIGNED>(P.x, t0 + 8 * j + g, k, P.T, P.K);
+            }
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const uint4 w0 = codes_of(w[a][0]), w1 = codes_of(w[a][1]);
-            uint4 xc[NT];
+            for (int a = 0; a < AHEAD; ++a) {
+                const uint4 w0 = codes_of(w[a][0]), w1 = codes_of(w[a][1]);
+                uint4 xc[NT];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) xc[j] = token_codes<ALIGNED>(x[a][j], k0 + a * step + 16 * q, P.K);
+                for (int j = 0; j < NT; ++j) xc[j] = token_codes<ALIGNED>(x[a][j], k0 + a * step + 16 * q, P.K);
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                uint32_t l0, h0, l1, h1;
-                widen4(word_of(w0, f), l0, h0);
-                widen4(word_of(w1, f), l1, h1);
+                for (int f = 0; f < 4; ++f) {
+                    uint32_t l0, h0, l1, h1;
+                    widen4(word_of(w0, f), l0, h0);
+                    widen4(word_of(w1, f), l1, h1);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    uint32_t xl, xh;
-                    widen4(word_of(xc[j], f), xl, xh);
-                    mma_f16(acc[j], l0, l1, h0, h1, xl, xh);
+                    for (int j = 0; j < NT; ++j) {
+                        uint32_t xl, xh;
+                        widen4(word_of(xc[j], f), xl, xh);
+                        mma_f16(acc[j], l0, l1, h0, h1, xl, xh);
+                    }
                 }
             }
         }
+        // acc[j]: outputs g and g + 8, tokens 8 j + 2 q and + 1
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float &sum = mine[(8 * j + 2 * q + (c & 1)) * kPitch + g + 8 * (c >> 1)];
+                sum = part == 0 ? acc[j][c] : __fadd_rn(sum, acc[j][c]);
+            }
     }
-    // acc[j]: outputs g and g + 8, tokens 8 j + 2 q and + 1
-    float *mine = sums + warp * kTok * kPitch;
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mine[(8 * j + 2 * q + (c & 1)) * kPitch + g + 8 * (c >> 1)] = acc[j][c];
     __syncthreads();
     for (int i = threadIdx.x; i < kTok * kOut; i += 32 * kFewWarps) {
         const uint64_t t = t0 + i / kOut, n = n0 + i % kOut;

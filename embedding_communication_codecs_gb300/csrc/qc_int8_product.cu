@@ -613,20 +613,24 @@ cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
 }
 
 // Which kernel multiplies T tokens: the weights are read as codes by qc_int8_few.cu up
-// to kFewTokens and by qc_int8_wide.cu up to kWideAny, or kWideTokens if the weights are
-// few and lie as TMA reads them (else they are copied first); beyond, both operands are
-// widened in memory and this file's tiles multiply them.  Weights of 4096 x 4096: 16 tokens
-// take 7 us against the next kernel's 10, 256 take 18.6 us against 22.7, 512 27 against 28.6,
-// and 1024 33 against 63.  11000 x 4096: 384 tokens 52 us against 66, 512 74 against 67.
-// Copied, 4096 x 4097: 384 tokens 29 us against 35, and 4096 x 1025 with 512 17 against 14.
-constexpr uint64_t kFewTokens = 16, kWideAny = 384, kWideTokens = 512;
-constexpr uint64_t kFewWeights = 1u << 25;
+// to kFewTokens.  Up to kWideAny qc_int8_wide.cu reads them so; up to kWideInPlace if the
+// weights are few and lie as TMA reads them (else they are copied first); and up to kWideMost
+// if the whole product is small.  Beyond, both operands are widened in memory and this
+// file's tiles multiply them.  Weights of 4096 x 4096: 16 tokens take 7 us against the next
+// kernel's 10, 256 take 18.6 us against 22.7, 512 27 against 28.6, and 1024 33 against 52.
+// 11000 x 4096: 384 tokens 52 us against 66, 512 74 against 67.  Copied, 4096 x 4097: 384
+// tokens 29 us against 35, and 4096 x 1025 with 512 17 against 14.  Small: 1024 x 1024, 1024
+// tokens 8.3 us against 11.1, 1531 x 2052 (copied) 640 tokens 15.3 against 19.4, but 2048 x
+// 2048, 896 tokens 17.1 against 15.7.
+constexpr uint64_t kFewTokens = 16, kWideAny = 384, kWideInPlace = 512, kWideMost = 2048;
+constexpr uint64_t kFewWeights = 1u << 25, kSmallProduct = 2500000000;
 
-bool wide_in_place(uint64_t T, uint64_t N, uint64_t K) { return T <= kWideTokens && N * K <= kFewWeights; }
+bool wide_always(uint64_t T, uint64_t N, uint64_t K) { return T <= kWideAny || (T <= kWideMost && T * N * K <= kSmallProduct); }
+bool wide_in_place(uint64_t T, uint64_t N, uint64_t K) { return T <= kWideInPlace && N * K <= kFewWeights; }
 
 size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K) {
     if (T <= kFewTokens) return 0;
-    if (T <= kWideAny) return wide_tokens_workspace(T, N, K);
+    if (wide_always(T, N, K)) return wide_tokens_workspace(T, N, K);
     const size_t tiles = widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K);
     return wide_in_place(T, N, K) ? std::max(tiles, wide_tokens_workspace(T, N, K)) : tiles;
 }
@@ -639,7 +643,7 @@ size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
     if (p.T <= kFewTokens) return launch_int8_few(p, stream);
-    if (p.T <= kWideAny || (wide_in_place(p.T, p.N, p.K) && wide_tokens_readable(p))) return launch_int8_wide(p, stream);
+    if (wide_always(p.T, p.N, p.K) || (wide_in_place(p.T, p.N, p.K) && wide_tokens_readable(p))) return launch_int8_wide(p, stream);
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     const Widen x{p.x_codes, nullptr, p.T, ws}, w{p.w_codes, nullptr, p.N, ws + widened_bytes(p.T, p.K)};
     const cudaError_t e = widen(p.K, x, w, stream);

@@ -14,7 +14,7 @@
 // instructions, and warps 4 to 15 widen and, at the end, store: three groups of four
 // (a warp reaches 32 lanes of tensor memory) take every third step, so that the
 // latency of a step, several hundred cycles of waits and conversions, is paid three
-// at a time.  Tensor memory (64 columns a step next to BT columns of sums) and shared
+// at a time.  Tensor memory (64 columns a step next to the columns of the sums) and shared
 // memory bound the ring of kRing widened steps, and the waits its ratio to the stages.
 // The lanes of a storing warp hold neighbouring outputs of one token, so its stores
 // are whole lines wherever y's rows start.
@@ -38,16 +38,25 @@ constexpr int kThreads = 512, kGroups = 3;
 // All of tensor memory, so it starts at column 0: the sums there, the ring at the end.
 constexpr int kACols = kStepK / 2, kTmemCols = 512;
 
+constexpr int kPartSteps = 16;
+constexpr uint64_t max_steps(int bt) { return bt == 48 ? 48 : bt == 64 ? 64 : 32; }
+
 template <int BT>
 struct Wide {
     static constexpr int kBytesW = kRows * kStepK, kBytesX = BT * kStepK;  // codes of a step
     static constexpr int kCodes = kBytesW + kBytesX;
     static constexpr int kBytesF = BT * kStepK * 2;                       // widened tokens of a step
     static constexpr int kRing = BT == 32 ? 7 : BT == 48 ? 5 : BT == 64 ? 4 : BT == 96 ? 4 : 3;
-    static constexpr int kStages = BT == 32 ? 8 : BT == 48 ? 7 : BT == 64 ? 6 : BT == 96 ? 4 : 3;
+    static constexpr int kStages = BT == 32 ? 8 : BT == 48 ? 7 : BT == 64 ? 6 : 4;
     static constexpr int kFirstA = kTmemCols - kRing * kACols;
+    // The tensor core's running sum loses up to a unit in the last place per instruction,
+    // always towards zero: codes of one sign are 5e-5 off after 16384 terms, 3e-6 after 4096.  A
+    // sum is cut into parts of 16 steps = 2048 terms, each in columns of its own, added in
+    // fp32 as they are stored; a unit has no more steps than there is room for parts.
+    static constexpr int kSumCols = BT == 32 ? 32 : BT <= 64 ? 64 : 128;
+    static constexpr int kSums = kFirstA / kSumCols;
     static constexpr int kSmem = kStages * kCodes + kRing * kBytesF + 1024;
-    static_assert(kFirstA >= BT, "the sums and the ring share tensor memory");
+    static_assert(kSums >= 2 && kSums * kPartSteps == max_steps(BT), "the sums and the ring share tensor memory");
     // A barrier's wait tells a phase from the one before it, not from the one before
     // that.  A group at step i has passed step i - kGroups, whose slot was freed by step
     // i - kGroups - kRing, and the instructions go in order: so the slot's last phase but one
@@ -162,7 +171,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (issues) {
 #pragma unroll
                     for (int j = 0; j < kStepK / 16; ++j)
-                        mma_tmem(0, C::kFirstA + r * kACols + 8 * j, (j < 4 ? b0 : b1) + (j & 3) * 2, kInstr, k > 0 || j > 0);
+                        mma_tmem(k / kPartSteps * C::kSumCols, C::kFirstA + r * kACols + 8 * j, (j < 4 ? b0 : b1) + (j & 3) * 2, kInstr,
+                                 k % kPartSteps > 0 || j > 0);
                     mma_commit(&freed[r]);
                 }
                 __syncwarp();
@@ -203,8 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);  // the whole warp has read its codes
                 tc_fence_after();
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -232,6 +240,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4 *>(at + (((2 * (p & 3) + 1) ^ (t & 7)) << 4)) = hi;
                 }
                 fence_proxy_async_shared();
+                // The stage is given back only here, where its codes have been widened and stored.
+                // Given back right after the loads, before their values were used, it was refilled
+                // under some of them (measured: wrong tokens in tiles of 64); tiles of 96 and 128 run
+                // 3 % slower for it.
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[s]);
                 tmem_wait_store();
                 tc_fence_before();
                 __syncwarp();
@@ -251,6 +265,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t v[8];
                 tmem_load8(mine + c, v);
                 tmem_wait_load();
+                for (uint32_t part = 1; part * kPartSteps < w.steps; ++part) {
+                    uint32_t more[8];
+                    tmem_load8(mine + part * C::kSumCols + c, more);
+                    tmem_wait_load();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(more[j])));
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float xt = __shfl_sync(kFull, xs[c / 32], (c + j) & 31);
@@ -295,7 +316,7 @@ struct WidePlan {
 // 512 tokens): 5 % off on average, and the choice within 3 % of the best.  Small weights
 // want many narrow tiles (1024 x 1024, 128 tokens: 6.7 us in tiles of 32, 11.4 in one of 128),
 // large ones as few as there are (16384 x 4096: 27.9 us in one, 33.8 in two of 64).  The
-// contraction is cut only as far as one unit for each SM.
+// contraction is cut only as far as one unit for each SM, or as the parts of a sum need.
 WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     constexpr uint64_t kBlocks = 152;
     const uint64_t steps = (K + kStepK - 1) / kStepK;
@@ -303,7 +324,8 @@ WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     double best_cost = 1e300;
     for (const int bt : {32, 48, 64, 96, 128}) {
         const uint64_t tiles = ((T + bt - 1) / bt) * ((N + kRows - 1) / kRows);
-        for (uint64_t s = 1; s == 1 || (s <= 16 && steps / s >= 2 && tiles * s <= kBlocks); ++s) {
+        const uint64_t least = (steps + max_steps(bt) - 1) / max_steps(bt);
+        for (uint64_t s = least; s == least || (s <= 16 && steps / s >= 2 && tiles * s <= kBlocks); ++s) {
             const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
             const uint64_t waves = (tiles * splits + kBlocks - 1) / kBlocks;
             double cost = static_cast<double>(waves) * (static_cast<double>(per) * (240 + 2.6 * bt) + 300 + 21.0 * bt);

@@ -144,7 +144,8 @@ PRODUCTS = [(1, 1, 1), (1, 64, 64), (1, 257, 4096), (1, 33, 1001), (2, 16, 32), 
             (7, 64, 2056), (8, 500, 1504), (9, 129, 96), (16, 256, 1024), (17, 40, 333), (24, 1100, 640),
             (31, 65, 130), (33, 128, 257), (48, 1000, 512), (64, 256, 256), (65, 77, 1000), (100, 300, 200),
             (128, 128, 64), (129, 257, 385), (200, 1031, 72), (255, 256, 1000), (256, 512, 2048),
-            (300, 520, 1030), (513, 768, 1025), (1000, 264, 520)]
+            (300, 520, 1030), (513, 768, 1025), (1000, 264, 520), (2049, 130, 261),
+            (2050, 66, 2500), (2100, 328, 136)]
 
 
 def int_case(T, N, K, kind):
@@ -530,6 +531,38 @@ def test_long_sums_keep_their_precision(q):
     want = dy.double().t() @ by_torch(xc, xs)
     # 2048 / 16 additions of at most 2^-23 of a sum no larger than the result, plus the joins
     assert float((dw.double() - want).norm() / want.norm()) <= (2048 / 16 + 8 + 16) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("T,N,K", [(300, 10000, 1024), (128, 33000, 1024), (96, 33000, 1024), (64, 33000, 4096),
+                                   (48, 33000, 1024), (32, 33000, 1024)])
+def test_many_units_many_times(q, T, N, K):
+    """Every token tile with several units to a block and the memory busy, fifty times: the
+    stages of codes are refilled as fast as they are given back."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    lim = 127 if K <= 1024 else 31
+    x = torch.randint(-lim, lim + 1, (T, K), generator=gen, device="cuda").to(torch.int8)
+    w = torch.randint(-lim, lim + 1, (N, K), generator=gen, device="cuda").to(torch.int8)
+    one_t, one_n = torch.ones(T, device="cuda"), torch.ones(N, device="cuda")
+    want = (x.double() @ w.double().t()).float()
+    for _ in range(50):
+        assert torch.equal(q.int8_matmul(x, one_t, w, one_n, dtype=F32), want)
+    assert q.qc_take_device_errors() == 0
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 300, 131072), (12, 300, 131072), (30, 20000, 16384), (48, 20000, 16384), (64, 20000, 16384),
+                                   (96, 20000, 16384), (128, 20000, 16384), (300, 20000, 16384), (700, 2000, 16384)])
+def test_sums_of_one_sign_keep_their_precision(q, T, N, K):
+    """Codes of 64 to 127 only, whose sums pass 2^24: each part of 2048 terms is 128 additions
+    that lose at most a unit in the last place of a sum no larger than the result; the
+    parts (up to 64) are added in fp32, and the scales are ones."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randint(64, 128, (T, K), generator=gen, device="cuda", dtype=torch.int8)
+    w = torch.randint(64, 128, (N, K), generator=gen, device="cuda", dtype=torch.int8)
+    y = q.int8_matmul(x, torch.ones(T, device="cuda"), w, torch.ones(N, device="cuda"), dtype=F32)
+    for part in (slice(0, 200), slice(N - 200, N)):
+        want = x.double() @ w[part].double().t()
+        assert bool(((y[:, part].double() - want).abs() <= (128 + 64) * 2.0 ** -23 * want).all())
+    assert q.qc_take_device_errors() == 0
 
 
 # ------------------------------------------------------------ how it is run

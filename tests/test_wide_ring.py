@@ -21,7 +21,7 @@ def constants():
     def of(name):
         text_of = re.search(name + r" = ((?:BT == \d+ \? \d+ : )+)(\d+);", text)
         lengths = {int(t): int(n) for t, n in re.findall(r"BT == (\d+) \? (\d+)", text_of.group(1))}
-        return {**lengths, 128: int(text_of.group(2))}
+        return {t: lengths.get(t, int(text_of.group(2))) for t in (32, 48, 64, 96, 128)}
     return groups, of("kRing"), of("kStages")
 
 
