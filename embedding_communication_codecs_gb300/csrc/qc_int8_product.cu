@@ -617,8 +617,8 @@ cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
 // weights are few and lie as TMA reads them (else they are copied first); and up to kWideMost
 // if the whole product is small.  Beyond, both operands are widened in memory and this
 // file's tiles multiply them.  Weights of 4096 x 4096: 16 tokens take 7 us against the next
-// kernel's 10, 256 take 18.6 us against 22.7, 512 27 against 28.6, and 1024 33 against 52.
-// 11000 x 4096: 384 tokens 52 us against 66, 512 74 against 67.  Copied, 4096 x 4097: 384
+// kernel's 10, 256 take 19.2 us against 22.7, 512 28.2 against 28.6, and 1024 34 against 52.
+// 11000 x 4096: 384 tokens 55 us against 66, 512 74 against 67.  Copied, 4096 x 4097: 384
 // tokens 29 us against 35, and 4096 x 1025 with 512 17 against 14.  Small: 1024 x 1024, 1024
 // tokens 8.3 us against 11.1, 1531 x 2052 (copied) 640 tokens 15.3 against 19.4, but 2048 x
 // 2048, 896 tokens 17.1 against 15.7.

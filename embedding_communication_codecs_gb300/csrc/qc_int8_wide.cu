@@ -39,21 +39,21 @@ constexpr int kThreads = 512, kGroups = 3;
 constexpr int kACols = kStepK / 2, kTmemCols = 512;
 
 constexpr int kPartSteps = 16;
-constexpr uint64_t max_steps(int bt) { return bt == 48 ? 48 : bt == 64 ? 64 : 32; }
+constexpr uint64_t max_steps(int bt) { return bt == 48 || bt == 96 ? 48 : bt == 64 ? 64 : 32; }
 
 template <int BT>
 struct Wide {
     static constexpr int kBytesW = kRows * kStepK, kBytesX = BT * kStepK;  // codes of a step
     static constexpr int kCodes = kBytesW + kBytesX;
     static constexpr int kBytesF = BT * kStepK * 2;                       // widened tokens of a step
-    static constexpr int kRing = BT == 32 ? 7 : BT == 48 ? 5 : BT == 64 ? 4 : BT == 96 ? 4 : 3;
-    static constexpr int kStages = BT == 32 ? 8 : BT == 48 ? 7 : BT == 64 ? 6 : 4;
+    static constexpr int kRing = BT == 32 ? 7 : BT == 48 ? 5 : BT == 64 ? 4 : 3;
+    static constexpr int kStages = BT == 32 ? 8 : BT == 48 ? 7 : BT == 64 ? 6 : BT == 96 ? 5 : 4;
     static constexpr int kFirstA = kTmemCols - kRing * kACols;
     // The tensor core's running sum loses up to a unit in the last place per instruction,
     // always towards zero: codes of one sign are 5e-5 off after 16384 terms, 3e-6 after 4096.  A
     // sum is cut into parts of 16 steps = 2048 terms, each in columns of its own, added in
     // fp32 as they are stored; a unit has no more steps than there is room for parts.
-    static constexpr int kSumCols = BT == 32 ? 32 : BT <= 64 ? 64 : 128;
+    static constexpr int kSumCols = (BT + 31) / 32 * 32;
     static constexpr int kSums = kFirstA / kSumCols;
     static constexpr int kSmem = kStages * kCodes + kRing * kBytesF + 1024;
     static_assert(kSums >= 2 && kSums * kPartSteps == max_steps(BT), "the sums and the ring share tensor memory");
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_shared();
                 // The stage is given back only here, where its codes have been widened and stored.
                 // Given back right after the loads, before their values were used, it was refilled
-                // under some of them (measured: wrong tokens in tiles of 64); tiles of 96 and 128 run
-                // 3 % slower for it.
+                // under some of them (measured: wrong tokens in tiles of 64); 16384 x 4096
+                // with 64 tokens takes 20 us either way, with 128 30.5 us against 27.8.
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
                 tmem_wait_store();
@@ -310,13 +310,12 @@ struct WidePlan {
 };
 
 // The token tile and the cuts of the contraction that cost least, in ns.  A step takes
-// longer the wider the tile, as shared memory carries the tokens four times (codes in and
-// out, f16 in and out); a unit starts and stores; a join is a launch and its sums written
+// longer the wider the tile, as its tokens are widened with it; a unit starts and stores; a join is a launch and its sums written
 // and read.  The figures were fitted to 1450 timed plans (1024 x 1024 to 16384 x 4096, 24 to
 // 512 tokens): 5 % off on average, and the choice within 3 % of the best.  Small weights
-// want many narrow tiles (1024 x 1024, 128 tokens: 6.7 us in tiles of 32, 11.4 in one of 128),
-// large ones as few as there are (16384 x 4096: 27.9 us in one, 33.8 in two of 64).  The
-// contraction is cut only as far as one unit for each SM, or as the parts of a sum need.
+// want many narrow tiles (1024 x 1024, 128 tokens: 6.5 us in tiles of 32, 11.4 in one of 128),
+// large ones as few as there are (16384 x 4096: 30.5 us in one, 33.8 in two of 64).  The
+// contraction is cut as far as two units for each SM, or as the parts of a sum need.
 WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     constexpr uint64_t kBlocks = 152;
     const uint64_t steps = (K + kStepK - 1) / kStepK;
@@ -325,7 +324,7 @@ WidePlan wide_plan(uint64_t T, uint64_t N, uint64_t K) {
     for (const int bt : {32, 48, 64, 96, 128}) {
         const uint64_t tiles = ((T + bt - 1) / bt) * ((N + kRows - 1) / kRows);
         const uint64_t least = (steps + max_steps(bt) - 1) / max_steps(bt);
-        for (uint64_t s = least; s == least || (s <= 16 && steps / s >= 2 && tiles * s <= kBlocks); ++s) {
+        for (uint64_t s = least; s == least || (s <= 16 && steps / s >= 2 && tiles * s <= 2 * kBlocks); ++s) {
             const uint64_t per = (steps + s - 1) / s, splits = (steps + per - 1) / per;
             const uint64_t waves = (tiles * splits + kBlocks - 1) / kBlocks;
             double cost = static_cast<double>(waves) * (static_cast<double>(per) * (240 + 2.6 * bt) + 300 + 21.0 * bt);
