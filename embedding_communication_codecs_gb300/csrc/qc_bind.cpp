@@ -2,14 +2,15 @@
 // tensors and the C ABI.
 //
 // Each function takes plainly right arguments (dense tensors of the expected types and
-// shapes on a CUDA device), allocates the results and the workspace, and makes the C
-// call on the current stream of the tensors' device.  It returns the results; None
+// shapes, all on one CUDA device), allocates the results and the workspace, and makes
+// the C call with that device current, on that device's current stream.  It returns the results; None
 // where an argument is anything else, for the caller to look closer; or the C call's
 // status where that is not QC_OK.  A call of a few microseconds on the GPU costs the
 // host about as much: through Python attributes and ctypes, a one-token product took
 // 12.6 us to issue, of which the C call is 3.1.
 #include <ATen/ATen.h>
 #include <Python.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -28,9 +29,12 @@ bool rows(const at::Tensor *t) {
     return t && (dense(*t, at::kBFloat16, 2) || dense(*t, at::kFloat, 2));
 }
 
+// Two tensors on the same device.
+bool together(const at::Tensor &a, const at::Tensor &b) { return a.device() == b.device(); }
+
 // Row codes and their scales.
 bool codes(const at::Tensor *c, const at::Tensor *s) {
-    return c && s && dense(*c, at::kChar, 2) && dense(*s, at::kFloat, 1) && s->size(0) == c->size(0);
+    return c && s && dense(*c, at::kChar, 2) && dense(*s, at::kFloat, 1) && s->size(0) == c->size(0) && together(*c, *s);
 }
 
 qc_dtype type_of(const at::Tensor &t) { return t.scalar_type() == at::kFloat ? QC_DTYPE_F32 : QC_DTYPE_BF16; }
@@ -73,6 +77,7 @@ PyObject *rowwise_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *x = n == 1 ? tensor(a[0]) : nullptr;
     if (!rows(x)) return none();
     const int64_t r = x->size(0), d = x->size(1);
+    const c10::cuda::CUDAGuard current(x->device());
     const at::Tensor c = make(*x, {r, d}, at::kChar), s = make(*x, {r}, at::kFloat);
     const qc_status st = qc_rowwise_int8(x->data_ptr(), type_of(*x), d, r, d, c.data_ptr<int8_t>(), s.data_ptr<float>(), stream_of(*x));
     if (st != QC_OK) return PyLong_FromLong(st);
@@ -87,6 +92,7 @@ PyObject *rowwise_int8_dequant(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!codes(c, s)) return none();
     const bool bf16 = a[2] == Py_True;
     const int64_t r = c->size(0), d = c->size(1);
+    const c10::cuda::CUDAGuard current(c->device());
     const at::Tensor out = results(*c, {r, d}, bf16);
     return answer(qc_rowwise_int8_dequant(c->data_ptr<int8_t>(), s->data_ptr<float>(), r, d, out.data_ptr(),
                                           bf16 ? QC_DTYPE_BF16 : QC_DTYPE_F32, d, stream_of(*c)), out);
@@ -108,10 +114,11 @@ PyObject *int8_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 6) return none();
     const at::Tensor *xc = tensor(a[0]), *xs = tensor(a[1]), *wc = tensor(a[2]), *ws = tensor(a[3]);
     const at::Tensor *bias = a[4] == Py_None ? nullptr : tensor(a[4]);
-    if (!codes(xc, xs) || !codes(wc, ws) || xc->size(1) != wc->size(1)) return none();
+    if (!codes(xc, xs) || !codes(wc, ws) || xc->size(1) != wc->size(1) || !together(*xc, *wc)) return none();
     const int64_t T = xc->size(0), N = wc->size(0), K = xc->size(1);
-    if (a[4] != Py_None && !(bias && dense(*bias, at::kFloat, 1) && bias->size(0) == N)) return none();
+    if (a[4] != Py_None && !(bias && dense(*bias, at::kFloat, 1) && bias->size(0) == N && together(*xc, *bias))) return none();
     const bool bf16 = a[5] == Py_True;
+    const c10::cuda::CUDAGuard current(xc->device());
     const at::Tensor y = results(*xc, {T, N}, bf16);
     const Workspace w(*xc, qc_int8_matmul_workspace(T, N, K));
     return answer(qc_int8_matmul(xc->data_ptr<int8_t>(), xs->data_ptr<float>(), wc->data_ptr<int8_t>(), ws->data_ptr<float>(),
@@ -124,9 +131,10 @@ PyObject *int8_input_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     QC_GUARD_BEGIN
     if (n != 4) return none();
     const at::Tensor *dy = tensor(a[0]), *wc = tensor(a[1]), *ws = tensor(a[2]);
-    if (!dy || !dense(*dy, at::kBFloat16, 2) || !codes(wc, ws) || dy->size(1) != wc->size(0)) return none();
+    if (!dy || !dense(*dy, at::kBFloat16, 2) || !codes(wc, ws) || dy->size(1) != wc->size(0) || !together(*dy, *wc)) return none();
     const int64_t T = dy->size(0), N = wc->size(0), K = wc->size(1);
     const bool bf16 = a[3] == Py_True;
+    const c10::cuda::CUDAGuard current(dy->device());
     const at::Tensor dx = results(*dy, {T, K}, bf16);
     const Workspace w(*dy, qc_int8_input_grad_workspace(T, N, K));
     return answer(qc_int8_input_grad(dy->data_ptr(), N, wc->data_ptr<int8_t>(), ws->data_ptr<float>(), T, N, K, dx.data_ptr(),
@@ -138,9 +146,10 @@ PyObject *int8_weight_grad(PyObject *, PyObject *const *a, Py_ssize_t n) {
     QC_GUARD_BEGIN
     if (n != 5) return none();
     const at::Tensor *dy = tensor(a[0]), *xc = tensor(a[1]), *xs = tensor(a[2]);
-    if (!dy || !dense(*dy, at::kBFloat16, 2) || !codes(xc, xs) || dy->size(0) != xc->size(0)) return none();
+    if (!dy || !dense(*dy, at::kBFloat16, 2) || !codes(xc, xs) || dy->size(0) != xc->size(0) || !together(*dy, *xc)) return none();
     const int64_t T = dy->size(0), N = dy->size(1), K = xc->size(1);
     const bool bf16 = a[3] == Py_True, with_bias = a[4] == Py_True;
+    const c10::cuda::CUDAGuard current(dy->device());
     const at::Tensor dw = results(*dy, {N, K}, bf16), db = with_bias ? make(*dy, {N}, at::kFloat) : at::Tensor();
     const Workspace w(*dy, qc_int8_weight_grad_workspace(T, N, K));
     const qc_status st = qc_int8_weight_grad(dy->data_ptr(), N, xc->data_ptr<int8_t>(), xs->data_ptr<float>(), T, N, K,
@@ -159,6 +168,7 @@ PyObject *swiglu_encode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *x = n == 1 ? tensor(a[0]) : nullptr;
     if (!rows(x) || x->size(1) % 2) return none();
     const int64_t r = x->size(0), two = x->size(1), d = two / 2;
+    const c10::cuda::CUDAGuard current(x->device());
     const at::Tensor hc = make(*x, {r, d}, at::kChar), hs = make(*x, {r}, at::kFloat), sc = make(*x, {r, two}, at::kChar),
                      ss = make(*x, {r, 2}, at::kFloat);
     const qc_status st = qc_swiglu_encode(x->data_ptr(), type_of(*x), two, r, d, hc.data_ptr<int8_t>(), hs.data_ptr<float>(),
@@ -176,6 +186,8 @@ PyObject *swiglu_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!rows(dh) || !sc || !ss || !dense(*sc, at::kChar, 2) || !dense(*ss, at::kFloat, 2)) return none();
     const int64_t r = dh->size(0), d = dh->size(1);
     if (sc->size(0) != r || sc->size(1) != 2 * d || ss->size(0) != r || ss->size(1) != 2) return none();
+    if (!together(*dh, *sc) || !together(*dh, *ss)) return none();
+    const c10::cuda::CUDAGuard current(dh->device());
     const at::Tensor out = make(*dh, {r, 2 * d}, dh->scalar_type());
     return answer(qc_swiglu_backward(dh->data_ptr(), type_of(*dh), d, sc->data_ptr<int8_t>(), ss->data_ptr<float>(), r, d,
                                      out.data_ptr(), 2 * d, stream_of(*dh)), out);
