@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ragged_swiglu_encode(const Swi
             m[0] = unit_max(g, m[0]);
             m[1] = unit_max(w, m[1]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) m[2] = max(m[2], abs_bits(swiglu(g.get(j), w.get(j))));
+            for (int j = 0; j < 8; ++j) m[2] = max(m[2], abs_bits(swiglu<T>(g.get(j), w.get(j))));
         }
         team_max(m, lanes, red, turn);
         if (!live) continue;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) ragged_swiglu_encode(const Swi
 #pragma unroll 1
         for (int e = lane8 - phase8(out); e < dim; e += step) {
             const auto g = load8_any<false>(gate, e, dim, begin, end), w = load8_any<false>(up, e, dim, begin, end);
-            encode_any(out, e, dim, sh, [&](int j) { return swiglu(g.get(j), w.get(j)); });
+            encode_any(out, e, dim, sh, [&](int j) { return swiglu<T>(g.get(j), w.get(j)); });
         }
     }
 }

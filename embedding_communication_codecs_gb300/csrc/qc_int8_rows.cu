@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) swiglu_encode(const SwigluPar
                     m[1] = unit_max(w[v], m[1]);
 #pragma unroll
                     for (int j = 0; j < U; ++j) {
-                        h[v][j] = swiglu(g[v].get(j), w[v].get(j));
+                        h[v][j] = swiglu<T>(g[v].get(j), w[v].get(j));
                         top = max_magnitude(top, h[v][j]);
                     }
                 }
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) swiglu_encode(const SwigluPar
             encode_rare_row<U>(saved, units, team.lane, lanes, sg.inverse, [=](uint32_t j) { return load_as_float(gate + j); });
             encode_rare_row<U>(saved + P.dim, units, team.lane, lanes, su.inverse, [=](uint32_t j) { return load_as_float(up + j); });
             encode_rare_row<U>(out, units, team.lane, lanes, sh.inverse,
-                               [=](uint32_t j) { return swiglu(load_as_float(gate + j), load_as_float(up + j)); });
+                               [=](uint32_t j) { return swiglu<T>(load_as_float(gate + j), load_as_float(up + j)); });
         } else if constexpr (HELD) {
             encode(0);
         } else {
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) swiglu_encode_ring(const Swig
                 m[1] = unit_max(b, m[1]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    h[v][j] = swiglu(a.get(j), b.get(j));
+                    h[v][j] = swiglu<T>(a.get(j), b.get(j));
                     top = max_magnitude(top, h[v][j]);
                 }
             }
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) swiglu_encode_ring(const Swig
             encode_rare_row<8>(saved, units, lane, lanes, sg.inverse, [=](uint32_t j) { return load_as_float(x + j); });
             encode_rare_row<8>(saved + P.dim, units, lane, lanes, su.inverse, [=](uint32_t j) { return load_as_float(y + j); });
             encode_rare_row<8>(out, units, lane, lanes, sh.inverse,
-                               [=](uint32_t j) { return swiglu(load_as_float(x + j), load_as_float(y + j)); });
+                               [=](uint32_t j) { return swiglu<T>(load_as_float(x + j), load_as_float(y + j)); });
             continue;
         }
 #pragma unroll
@@ -355,10 +355,11 @@ __global__ void __launch_bounds__(kRowThreads) swiglu_backward(const SwigluParam
                     for (int j = 0; j < U; ++j) {
                         const float g = __fmul_rn(cg[v].get(j), sg);
                         const float u = __fmul_rn(cu[v].get(j), su);
-                        const float x = d[v].get(j), sig = sigmoid(g);
-                        const float slope = __fmul_rn(sig, __fmaf_rn(g, __fsub_rn(1.0f, sig), 1.0f));
+                        const float x = d[v].get(j);
+                        const Sigma sig = sigma_of<T>(g);
+                        const float slope = __fmul_rn(sig.s, __fmaf_rn(g, sig.other, 1.0f));
                         dg[j] = __fmul_rn(__fmul_rn(x, u), slope);
-                        du[j] = __fmul_rn(x, __fmul_rn(g, sig));
+                        du[j] = __fmul_rn(x, __fmul_rn(g, sig.s));
                     }
                     store_values<T, U>(out + at, dg);
                     store_values<T, U>(out + P.dim + at, du);
