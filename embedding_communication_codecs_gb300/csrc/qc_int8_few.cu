@@ -190,11 +190,12 @@ __global__ void __launch_bounds__(32 * kFewWarps, BLOCKS) few_tokens(const FewPa
     for (int i = threadIdx.x; i < kTok * kOut; i += 32 * kFewWarps) {
         const uint64_t t = t0 + i / kOut, n = n0 + i % kOut;
         if (t >= P.T || n >= P.N) continue;
+        const float xs = __ldg(P.x_scale + t), ws = __ldg(P.w_scale + n), bias = P.bias ? __ldg(P.bias + n) : 0.0f;
         float v = 0.0f;
 #pragma unroll
         for (int s = 0; s < kFewWarps; ++s) v = __fadd_rn(v, sums[(s * kTok + i / kOut) * kPitch + i % kOut]);
-        v = __fmul_rn(v, __fmul_rn(__ldg(P.x_scale + t), __ldg(P.w_scale + n)));
-        if (P.bias) v = __fadd_rn(v, __ldg(P.bias + n));
+        v = far_scale(xs) || far_scale(ws) ? scaled_far(v, xs, ws) : __fmul_rn(v, __fmul_rn(xs, ws));
+        if (P.bias) v = __fadd_rn(v, bias);
         if (P.y_bf16)
             static_cast<uint16_t *>(P.y)[t * P.y_stride + n] = to_bf16(v);
         else

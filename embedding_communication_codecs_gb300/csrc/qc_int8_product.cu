@@ -133,6 +133,16 @@ __device__ __forceinline__ float4 finish4(const GemmParams &P, float ms, uint32_
     return make_float4(r[0], r[1], r[2], r[3]);
 }
 
+// Whether any scale of a warp's 32 rows and C columns is far (only the forward product, whose
+// operands are both K-major, has scales here).
+template <int C>
+__device__ __forceinline__ bool far_scales(const GemmParams &P, uint32_t m0, uint32_t n, int lane) {
+    bool far = far_scale(load_here(P.m_scale + min(m0 + lane, static_cast<uint32_t>(P.M) - 1)));
+#pragma unroll
+    for (int c = 0; c < C; c += 32) far |= far_scale(load_here(P.n_scale + min(n + c + lane, static_cast<uint32_t>(P.N) - 1)));
+    return __any_sync(kFull, far);
+}
+
 // A storing warp's C columns from n on of the 32 rows from m0 on (lane l holds row
 // m0 + l): scaled, biased, written to the warp's 4 KB of shared memory as 32 rows of
 // 128 bytes and stored from there by TMA.
@@ -170,10 +180,12 @@ __device__ __forceinline__ void store_tma(const GemmParams &P, const CUtensorMap
 }
 
 // The same, element by element: 32 x 32 sums through the warp's shared memory, so
-// that its lanes store neighbouring columns of one row.
+// that its lanes store neighbouring columns of one row.  Far scales are only multiplied
+// here: in store_tma() a test for each sum cost 8192 x 16384 x 4096 800 us instead of 580.
 template <int C>
 __device__ __forceinline__ void store_anywhere(const GemmParams &P, uint32_t m0, uint32_t n, int lane, uint8_t *buf,
-                                               const float (&acc)[C]) {
+                                               const float (&acc)[C], bool far) {
+    if (lane == 0) tma_store_wait_read();  // of an earlier tile, whose scales were not far
     const int rows = P.M - m0 < 32 ? static_cast<int>(P.M - m0) : 32;
 #pragma unroll
     for (int c = 0; c < C; c += 32) {
@@ -187,10 +199,10 @@ __device__ __forceinline__ void store_anywhere(const GemmParams &P, uint32_t m0,
         const uint32_t col = n + c + lane;
         if (col < P.N) {
             const float ns = P.m_scale ? __ldg(P.n_scale + col) : 1.0f, bias = P.bias ? __ldg(P.bias + col) : 0.0f;
-#pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
-                float v = *reinterpret_cast<const float *>(buf + swizzled(r, lane >> 2) + 4 * (lane & 3));
-                if (P.m_scale) v = __fmul_rn(v, __fmul_rn(__ldg(P.m_scale + m0 + r), ns));
+            const auto sum_at = [&](int r) {
+                return *reinterpret_cast<const float *>(buf + swizzled(r, lane >> 2) + 4 * (lane & 3));
+            };
+            const auto store = [&](int r, float v) {
                 if (P.bias) v = __fadd_rn(v, bias);
                 const uint64_t at = static_cast<uint64_t>(m0 + r) * P.out_stride + col;
                 if (P.out_bf16) {
@@ -198,6 +210,16 @@ __device__ __forceinline__ void store_anywhere(const GemmParams &P, uint32_t m0,
                 } else {
                     float *o = static_cast<float *>(P.out) + at;
                     *o = P.accumulate ? __fadd_rn(*o, v) : v;
+                }
+            };
+            if (far) {
+#pragma unroll 1
+                for (int r = 0; r < rows; ++r) store(r, scaled_far_call(sum_at(r), __ldg(P.m_scale + m0 + r), ns));
+            } else {
+#pragma unroll 4
+                for (int r = 0; r < rows; ++r) {
+                    const float v = sum_at(r);
+                    store(r, P.m_scale ? __fmul_rn(v, __fmul_rn(__ldg(P.m_scale + m0 + r), ns)) : v);
                 }
             }
         }
@@ -345,8 +367,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const Unit w = unit_at(u, tiles_m, tiles_n, P);
             const uint32_t m0 = w.m * kPairM + rank * kBlockM + quarter * 32, n = w.n * BN + c0;
             if (m0 >= P.M || n >= P.N) continue;
-            if constexpr (OUT == kAnywhere)
-                store_anywhere<T::kWarpCols>(P, m0, n, lane, buf, acc);
+            const bool far = !B_MN && OUT != kSums && far_scales<T::kWarpCols>(P, m0, n, lane);
+            if (OUT == kAnywhere || far)
+                store_anywhere<T::kWarpCols>(P, m0, n, lane, buf, acc, far);
             else
                 store_tma<T::kWarpCols, OUT>(P, map_out, w.split, m0, n, lane, buf, acc);
         }
@@ -376,7 +399,10 @@ __global__ void __launch_bounds__(256) join(const JoinParams P) {
         for (int j = 0; j < 4; ++j) {
             if (n + j >= P.N) break;
             float r = v[j];
-            if (P.m_scale) r = __fmul_rn(r, __fmul_rn(__ldg(P.m_scale + m), __ldg(P.n_scale + n + j)));
+            if (P.m_scale) {
+                const float ms = __ldg(P.m_scale + m), ns = __ldg(P.n_scale + n + j);
+                r = far_scale(ms) || far_scale(ns) ? scaled_far(r, ms, ns) : __fmul_rn(r, __fmul_rn(ms, ns));
+            }
             if (P.bias) r = __fadd_rn(r, __ldg(P.bias + n + j));
             if (P.out_bf16) {
                 static_cast<uint16_t *>(P.out)[m * P.out_stride + n + j] = to_bf16(r);

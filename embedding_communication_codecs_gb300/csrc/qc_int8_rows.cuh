@@ -166,6 +166,37 @@ __device__ __forceinline__ void store_values(T *p, const float (&v)[U]) {
     *reinterpret_cast<typename RawOf<T, U>::type *>(p) = r;
 }
 
+// A sum's two scales become one factor, v * (xs * ws), so that the sum is rounded once more.
+// Where the factor is subnormal or leaves fp32's range, which says nothing about the result,
+// the scales' fractions are multiplied and their exponents applied last.  Scales outside 2^-63 ..
+// 2^63, whose products may do so, are "far"; 0 is not (its products are 0 whatever the other
+// scale), nor is what is not finite.
+__device__ __forceinline__ bool far_scale(float s) {
+    const uint32_t e = (__float_as_uint(s) >> 23) & 0xFFu;
+    return (e < 64u || e > 190u) && e != 255u && s != 0.0f;
+}
+
+// s = fraction * 2^exponent, 1 <= |fraction| < 2; 0 and what is not finite as they are.
+__device__ __forceinline__ float fraction(float s, int &exponent) {
+    const bool small = fabsf(s) < 0x1p-126f;
+    const uint32_t b = __float_as_uint(small ? __fmul_rn(s, 0x1p24f) : s), e = (b >> 23) & 0xFFu;
+    exponent = 0;
+    if (e == 0u || e == 255u) return s;
+    exponent = static_cast<int>(e) - (small ? 151 : 127);
+    return __uint_as_float((b & 0x807FFFFFu) | 0x3F800000u);
+}
+
+// v is 0 or 1 <= |v| < 2^40.  Halves of the exponent have one sign, so only the last product
+// can leave the normal range.
+__device__ __forceinline__ float scaled_far(float v, float xs, float ws) {
+    int ex, ew;
+    const float p = __fmul_rn(v, __fmul_rn(fraction(xs, ex), fraction(ws, ew)));
+    const int e = max(-252, min(254, ex + ew)), half = e / 2;
+    return __fmul_rn(__fmul_rn(p, __int_as_float((127 + half) << 23)), __int_as_float((127 + e - half) << 23));
+}
+// The same as a call, to keep it out of unrolled loops.
+static __device__ __noinline__ float scaled_far_call(float v, float xs, float ws) { return scaled_far(v, xs, ws); }
+
 // A team of `lanes` threads (a power of two, 8 to THREADS) and the rows it owns.
 struct Team {
     uint32_t lanes, lane, first, stride;

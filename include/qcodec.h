@@ -426,9 +426,10 @@ qc_status qc_rowwise_int8_dequant(const int8_t *codes, const float *row_scale, s
                                   qc_stream_t stream);
 
 /*
- * qc_int8_matmul -- y_tn = (sum_k x_codes_tk * w_codes_nk) * (x_scale_t * w_scale_n) + bias_n
+ * qc_int8_matmul -- y_tn = (sum_k x_codes_tk * w_codes_nk) * x_scale_t * w_scale_n + bias_n
  * for any int8 codes and fp32 scales (one per token, one per output channel).
- * The sum is held in fp32 and is exact while its partial sums stay below 2^24.
+ * The sum is held in fp32 and is exact while its partial sums stay below 2^24; the scales
+ * are multiplied with each other first, without leaving fp32's range on the way.
  * x_codes : T x K.  w_codes : N x K.  bias : N fp32, or NULL.  y : T x N fp32 or bf16.
  */
 size_t qc_int8_matmul_workspace(size_t T, size_t N, size_t K);
