@@ -493,9 +493,22 @@ def decode_accumulate(codes, scale, offset, *, n, bits, bucket, scheme=QC_SCHEME
     return out
 
 
-# the 8-bit linear layer (needs the names above)
-from .layer import (int8_input_grad, int8_matmul, int8_weight_grad, qc_int8_input_grad,  # noqa: E402,F401
-                    qc_int8_input_grad_workspace, qc_int8_matmul, qc_int8_matmul_workspace,
-                    qc_int8_weight_grad, qc_int8_weight_grad_workspace, qc_rowwise_int8,
-                    qc_rowwise_int8_dequant, qc_swiglu_backward, qc_swiglu_encode, rowwise_int8,
-                    rowwise_int8_dequant, swiglu_backward, swiglu_encode)
+# The 8-bit linear layer is loaded with the first of its names: it needs torch, which
+# nothing above does before its first call.
+_LAYER = ("int8_input_grad", "int8_matmul", "int8_weight_grad", "qc_int8_input_grad", "qc_int8_input_grad_workspace",
+          "qc_int8_matmul", "qc_int8_matmul_workspace", "qc_int8_weight_grad", "qc_int8_weight_grad_workspace",
+          "qc_rowwise_int8", "qc_rowwise_int8_dequant", "qc_swiglu_backward", "qc_swiglu_encode", "rowwise_int8",
+          "rowwise_int8_dequant", "swiglu_backward", "swiglu_encode")
+
+
+def __getattr__(name):
+    if name != "layer" and name not in _LAYER:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    layer = importlib.import_module(".layer", __name__)
+    globals().update({n: getattr(layer, n) for n in _LAYER})
+    return layer if name == "layer" else globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_LAYER, "layer"})

@@ -1,5 +1,6 @@
 """Build libqcodec.so in-tree with nvcc for sm_103a, and the torch binding of the
-8-bit layer's calls (``_qcbind``) next to it with g++.
+8-bit layer's calls (``_qcbind``) next to it with g++ (left out where torch is not
+installed: only that layer needs it, and it can call the library through ctypes).
 
 Each CUDA translation unit is compiled to an object file in parallel, then the
 objects are linked into a shared library next to this file.  The CUDA runtime
@@ -20,6 +21,7 @@ LIB_NAME = "libqcodec.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 BIND_PATH = os.path.join(PKG, "_qcbind.so")
 BIND_SOURCE = "qc_bind.cpp"
+BIND_STAMP = os.path.join(PKG, "_qcbind.stamp")  # the torch and Python that _qcbind was compiled against
 SOURCES = ["qc_api.cu", "qc_encode.cu", "qc_encode_tma.cu", "qc_encode_clip.cu",
            "qc_encode_clip_bf16.cu", "qc_encode_bf16.cu", "qc_encode_bf16_fast.cu", "qc_decode.cu", "qc_decode_tma.cu",
            "qc_reencode.cu", "qc_reencode_other.cu", "qc_topk.cu", "qc_fp8.cu",
@@ -44,18 +46,44 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found; the CUDA toolkit is required to build libqcodec")
 
 
-def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [BIND_SOURCE]]
-    files.append(os.path.join(ROOT, "include", "qcodec.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _newer(path, sources) -> bool:
+    """path exists and is no older than its sources and this file."""
+    files = [*sources, os.path.join(ROOT, "include", "qcodec.h"), os.path.abspath(__file__)]
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in files)
+
+
+def bind_stamp():
+    """What an extension depends on besides its sources, without importing torch: where torch
+    lies, its version file, and the interpreter's ABI.  None where torch is not installed."""
+    import importlib.util
+    import sysconfig
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        return None
+    root = os.path.dirname(spec.origin)
+    with open(os.path.join(root, "version.py")) as f:
+        return "\n".join((root, str(sysconfig.get_config_var("SOABI")), f.read()))
+
+
+def bind_fits() -> bool:
+    """_qcbind was compiled against the torch and the Python that are here now."""
+    try:
+        with open(BIND_STAMP) as f:
+            return os.path.exists(BIND_PATH) and f.read() == bind_stamp()
+    except OSError:
+        return False
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB_PATH, [os.path.join(CSRC, s) for s in SOURCES + HEADERS])
+
+
+def bind_up_to_date() -> bool:
+    return bind_stamp() is None or (bind_fits() and _newer(BIND_PATH, [os.path.join(CSRC, BIND_SOURCE)]))
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(BIND_PATH)):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BIND_PATH))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
+    return library_up_to_date() and bind_up_to_date()
 
 
 def bind_flags():
@@ -72,16 +100,26 @@ def bind_flags():
             [f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"])
 
 
+def _link(cmd, path):
+    """Run the linker into a temporary file and put it in place in one step."""
+    tmp = path + f".tmp{os.getpid()}"
+    r = subprocess.run([*cmd[:2], "-o", tmp, *cmd[2:]], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+
+
 def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile and link libqcodec.so; returns its path."""
-    if not force and up_to_date():
+    """Compile and link libqcodec.so and the binding; returns the library's path."""
+    lib, bind = force or not library_up_to_date(), bind_stamp() is not None and (force or not bind_up_to_date())
+    if not lib and not bind:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
     def compile_one(src):
-        obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
+        obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
         cmd = [cc, *ARCH, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
@@ -98,26 +136,22 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool =
         return obj, libs
 
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        bind = ex.submit(compile_bind)
-        results = list(ex.map(compile_one, SOURCES))
-        bind_obj, bind_libs = bind.result()
-    if verbose or ptxas_info:
-        for _, log in results:
-            if log:
-                print(log)
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *[o for o, _ in results], "-cudart", "static",
-           "-Xlinker", f"-soname={LIB_NAME}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    tmp = BIND_PATH + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, bind_obj, LIB_PATH, "-Wl,-rpath,$ORIGIN", *bind_libs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BIND_PATH)
+        bound = ex.submit(compile_bind) if bind else None
+        results = list(ex.map(compile_one, SOURCES)) if lib else []
+        if verbose or ptxas_info:
+            for _, log in results:
+                if log:
+                    print(log)
+        # the library is in place whatever becomes of the binding
+        if lib:
+            _link([cc, "-shared", *ARCH, *[o for o, _ in results], "-cudart", "static", "-Xlinker", f"-soname={LIB_NAME}"],
+                  LIB_PATH)
+        if bind:
+            stamp = bind_stamp()
+            obj, libs = bound.result()
+            _link(["g++", "-shared", obj, LIB_PATH, "-Wl,-rpath,$ORIGIN", *libs], BIND_PATH)
+            with open(BIND_STAMP, "w") as f:
+                f.write(stamp)
     return LIB_PATH
 
 

@@ -15,12 +15,38 @@ stream they run on, and return the results.
 from __future__ import annotations
 
 import contextlib
+import warnings
 
 import torch
 
-from . import _qcbind
+from . import build
 from . import (QC_ACCUMULATE_INTO_OUT, QC_DTYPE_BF16, QC_DTYPE_F32, _check, _need, _on_device, _ptr,
                _stream, lib)
+
+
+
+class _Declines:
+    """In the binding's place where there is none: every call declines, and the code here makes
+    the same C call through ctypes."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _binding():
+    why = "it was compiled against another torch or Python"
+    if build.bind_fits():
+        try:
+            from . import _qcbind
+            return _qcbind
+        except ImportError as e:
+            why = str(e)
+    warnings.warn(f"the 8-bit layer's calls go through ctypes, at about 10 us more each: the binding {build.BIND_PATH} "
+                  f"does not load ({why}); build it with `python {build.__file__}`", RuntimeWarning, stacklevel=2)
+    return _Declines()
+
+
+_qcbind = _binding()
 
 _I8 = (torch.int8,)
 _F32 = (torch.float32,)
@@ -195,7 +221,8 @@ def qc_swiglu_backward(dh, dtype, dh_stride, saved_codes, saved_scale, rows, dim
 # Plainly right arguments (dense tensors of the expected types and shapes on a CUDA
 # device) go through the compiled binding, which allocates and calls the library
 # without Python in between.  Where it declines (None), the code here looks closer:
-# it accepts a strided matrix and says what is wrong with anything else.
+# it accepts a strided matrix and says what is wrong with anything else.  Without a
+# binding it makes every call.
 
 
 def _rows(t, name, dtypes):
@@ -293,13 +320,17 @@ def rowwise_int8_dequant(codes, row_scale, *, dtype=torch.bfloat16, stream=None)
     if stream is not None:
         with _on(stream, codes):
             return rowwise_int8_dequant(codes, row_scale, dtype=dtype)
-    _dtype(dtype)
+    code = _dtype(dtype)
     got = _qcbind.rowwise_int8_dequant(codes, row_scale, dtype is torch.bfloat16)
     if got is not None:
         return _done(got)
     _codes(codes, row_scale, "row")
-    _device_of(codes=codes, row_scale=row_scale)
-    raise ValueError("codes and row_scale are not usable")
+    rows, dim = codes.shape
+    with _device_of(codes=codes, row_scale=row_scale):
+        out = _empty(codes, rows, dim, dtype=dtype)
+        _check(lib.qc_rowwise_int8_dequant(codes.data_ptr(), row_scale.data_ptr(), rows, dim, out.data_ptr(), code, dim,
+                                           _current(codes)))
+    return out
 
 
 def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bfloat16, stream=None):
@@ -308,7 +339,7 @@ def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bf
     if stream is not None:
         with _on(stream, x_codes):
             return int8_matmul(x_codes, x_scale, w_codes, w_scale, bias, dtype=dtype)
-    _dtype(dtype)
+    code = _dtype(dtype)
     got = _qcbind.int8_matmul(x_codes, x_scale, w_codes, w_scale, bias, dtype is torch.bfloat16)
     if got is not None:
         return _done(got)
@@ -318,8 +349,15 @@ def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bf
         _dense(bias, "bias", _F32, (w_codes.shape[0],))
     if w_codes.shape[1] != x_codes.shape[1]:
         raise ValueError(f"w_codes has rows of {w_codes.shape[1]}, x_codes of {x_codes.shape[1]}")
-    _device_of(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias)
-    raise ValueError("the tensors are not usable")
+    T, K = x_codes.shape
+    N = w_codes.shape[0]
+    with _device_of(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias):
+        y = _empty(x_codes, T, N, dtype=dtype)
+        nbytes = lib.qc_int8_matmul_workspace(T, N, K)
+        ws = _scratch(x_codes, nbytes)
+        _check(lib.qc_int8_matmul(x_codes.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(), w_scale.data_ptr(), _ptr(bias),
+                                  T, N, K, y.data_ptr(), code, N, _ptr(ws), nbytes, _current(x_codes)))
+    return y
 
 
 def int8_input_grad(dy, w_codes, w_scale, *, dtype=torch.bfloat16, stream=None):
