@@ -44,7 +44,7 @@ STATUS_NAMES = {0: "QC_OK", 1: "QC_ERR_NULL", 2: "QC_ERR_INVALID_ARG", 3: "QC_ER
 EXPORTS = ("qc_code_words", "qc_num_buckets", "qc_encode_ef", "qc_encode_ef_segments",
            "qc_decode_accumulate",
            "qc_reencode", "qc_topk_encode_ef", "qc_topk_decode_accumulate", "qc_sign_vote", "qc_rowwise_fp8", "qc_rowwise_fp8_dequant",
-           "qc_rowwise_int8", "qc_rowwise_int8_dequant", "qc_int8_matmul_workspace", "qc_int8_matmul",
+           "qc_rowwise_int8", "qc_rowwise_int8_dequant", "qc_int8_matmul_workspace", "qc_int8_matmul_codes_workspace", "qc_int8_matmul",
            "qc_int8_input_grad_workspace", "qc_int8_input_grad", "qc_int8_weight_grad_workspace",
            "qc_int8_weight_grad", "qc_swiglu_encode", "qc_swiglu_backward", "qc_take_device_errors",
            "qc_set_status_word", "qc_selftest_wait_timeout",
@@ -92,6 +92,7 @@ def _load():
     for name in ("qc_int8_matmul_workspace", "qc_int8_input_grad_workspace",
                  "qc_int8_weight_grad_workspace"):
         getattr(lib, name).argtypes, getattr(lib, name).restype = [S, S, S], S
+    lib.qc_int8_matmul_codes_workspace.argtypes, lib.qc_int8_matmul_codes_workspace.restype = [P, P, S, S, S], S
     for name in ("qc_rowwise_int8", "qc_rowwise_int8_dequant", "qc_int8_matmul", "qc_int8_input_grad",
                  "qc_int8_weight_grad", "qc_swiglu_encode", "qc_swiglu_backward",
                  "qc_encode_ef", "qc_encode_ef_segments", "qc_decode_accumulate", "qc_reencode", "qc_topk_encode_ef",
@@ -496,7 +497,7 @@ def decode_accumulate(codes, scale, offset, *, n, bits, bucket, scheme=QC_SCHEME
 # The 8-bit linear layer is loaded with the first of its names: it needs torch, which
 # nothing above does before its first call.
 _LAYER = ("int8_input_grad", "int8_matmul", "int8_weight_grad", "qc_int8_input_grad", "qc_int8_input_grad_workspace",
-          "qc_int8_matmul", "qc_int8_matmul_workspace", "qc_int8_weight_grad", "qc_int8_weight_grad_workspace",
+          "qc_int8_matmul", "qc_int8_matmul_workspace", "qc_int8_matmul_codes_workspace", "qc_int8_weight_grad", "qc_int8_weight_grad_workspace",
           "qc_rowwise_int8", "qc_rowwise_int8_dequant", "qc_swiglu_backward", "qc_swiglu_encode", "rowwise_int8",
           "rowwise_int8_dequant", "swiglu_backward", "swiglu_encode")
 

@@ -1,6 +1,8 @@
 // qc_api_layer.cu -- the C ABI of the 8-bit linear layer (declared in
 // include/qcodec.h): host-side validation and dispatch.  As in qc_api.cu,
 // every argument error is reported before any CUDA call.
+#include <algorithm>
+
 #include "../../include/qcodec.h"
 #include "qc_api_util.h"
 #include "qc_internal.h"
@@ -209,7 +211,14 @@ qc_status qc_swiglu_backward(const void *dh, qc_dtype dtype, size_t dh_stride,
 }
 
 size_t qc_int8_matmul_workspace(size_t T, size_t N, size_t K) {
-    return check_product("qc_int8_matmul_workspace", T, N, K) == QC_OK ? qc::int8_matmul_workspace(T, N, K) : 0;
+    if (check_product("qc_int8_matmul_workspace", T, N, K) != QC_OK) return 0;
+    const size_t any = qc::int8_matmul_workspace(T, N, K, false);
+    return K % 16 ? any : std::max(any, qc::int8_matmul_workspace(T, N, K, true));
+}
+
+size_t qc_int8_matmul_codes_workspace(const int8_t *x_codes, const int8_t *w_codes, size_t T, size_t N, size_t K) {
+    if (check_product("qc_int8_matmul_codes_workspace", T, N, K) != QC_OK) return 0;
+    return qc::int8_matmul_workspace(T, N, K, qc::wide_tokens_readable(x_codes, w_codes, K));
 }
 
 size_t qc_int8_input_grad_workspace(size_t T, size_t N, size_t K) {
@@ -231,7 +240,7 @@ qc_status qc_int8_matmul(const int8_t *x_codes, const float *x_scale, const int8
     QC_TRY(check_product(fn, T, N, K));
     if (T == 0) return ok();
     QC_TRY(check_stride(fn, "y_stride", y_stride, N, T));
-    const size_t es = size_of(y_dtype), need = qc::int8_matmul_workspace(T, N, K);
+    const size_t es = size_of(y_dtype), need = qc::int8_matmul_workspace(T, N, K, qc::wide_tokens_readable(x_codes, w_codes, K));
     QC_TRY(check_workspace_size(fn, workspace_bytes, need));
     const Buffer b[] = {{"x_codes", x_codes, T * K, 1, false},
                         {"x_scale", x_scale, T * 4, 4, false},

@@ -120,7 +120,7 @@ PyObject *int8_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const bool bf16 = a[5] == Py_True;
     const c10::cuda::CUDAGuard current(xc->device());
     const at::Tensor y = results(*xc, {T, N}, bf16);
-    const Workspace w(*xc, qc_int8_matmul_workspace(T, N, K));
+    const Workspace w(*xc, qc_int8_matmul_codes_workspace(xc->data_ptr<int8_t>(), wc->data_ptr<int8_t>(), T, N, K));
     return answer(qc_int8_matmul(xc->data_ptr<int8_t>(), xs->data_ptr<float>(), wc->data_ptr<int8_t>(), ws->data_ptr<float>(),
                                  bias ? bias->data_ptr<float>() : nullptr, T, N, K, y.data_ptr(),
                                  bf16 ? QC_DTYPE_BF16 : QC_DTYPE_F32, N, w.p(), w.bytes, stream_of(*xc)), y);

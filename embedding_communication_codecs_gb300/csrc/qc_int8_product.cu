@@ -654,11 +654,10 @@ constexpr uint64_t kFewWeights = 1u << 25, kSmallProduct = 2500000000;
 bool wide_always(uint64_t T, uint64_t N, uint64_t K) { return T <= kWideAny || (T <= kWideMost && T * N * K <= kSmallProduct); }
 bool wide_in_place(uint64_t T, uint64_t N, uint64_t K) { return T <= kWideInPlace && N * K <= kFewWeights; }
 
-size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K) {
+size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K, bool readable) {
     if (T <= kFewTokens) return 0;
-    if (wide_always(T, N, K)) return wide_tokens_workspace(T, N, K);
-    const size_t tiles = widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K);
-    return wide_in_place(T, N, K) ? std::max(tiles, wide_tokens_workspace(T, N, K)) : tiles;
+    if (wide_always(T, N, K) || (wide_in_place(T, N, K) && readable)) return wide_tokens_workspace(T, N, K, readable);
+    return widened_bytes(T, K) + widened_bytes(N, K) + partial_bytes(T, N, K);
 }
 size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
     return widened_bytes(N, K) + widened_bytes(T, N) + partial_bytes(T, K, N);
@@ -669,7 +668,7 @@ size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K) {
 
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream) {
     if (p.T <= kFewTokens) return launch_int8_few(p, stream);
-    if (wide_always(p.T, p.N, p.K) || (wide_in_place(p.T, p.N, p.K) && wide_tokens_readable(p))) return launch_int8_wide(p, stream);
+    if (wide_always(p.T, p.N, p.K) || (wide_in_place(p.T, p.N, p.K) && wide_tokens_readable(p.x_codes, p.w_codes, p.K))) return launch_int8_wide(p, stream);
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     const Widen x{p.x_codes, nullptr, p.T, ws}, w{p.w_codes, nullptr, p.N, ws + widened_bytes(p.T, p.K)};
     const cudaError_t e = widen(p.K, x, w, stream);

@@ -397,14 +397,15 @@ cudaError_t launch_wide(const ProductParams &p, const Codes &wc, const Codes &xc
 
 }  // namespace
 
-bool wide_tokens_readable(const ProductParams &p) { return readable(p.w_codes, p.K) && readable(p.x_codes, p.K); }
+bool wide_tokens_readable(const int8_t *x_codes, const int8_t *w_codes, uint64_t K) {
+    return readable(w_codes, K) && readable(x_codes, K);
+}
 
 // Room for the sums of a split contraction and, for codes that TMA cannot read where
-// they lie, for copies of both matrices.  The bases' alignment is not known here, so
-// the copies have room whatever K is.
-size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K) {
+// they lie, for copies of both matrices.
+size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K, bool readable) {
     const WidePlan plan = wide_plan(T, N, K);
-    return (plan.splits > 1 ? plan.splits * ceil32(T) * ceil32(N) * 4 : 0) + copied_bytes(N, K) + copied_bytes(T, K);
+    return (plan.splits > 1 ? plan.splits * ceil32(T) * ceil32(N) * 4 : 0) + (readable ? 0 : copied_bytes(N, K) + copied_bytes(T, K));
 }
 
 cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream) {
@@ -425,7 +426,7 @@ cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream) {
     w.status = p.status;
     Codes wc{p.w_codes, p.K}, xc{p.x_codes, p.K};
     cudaError_t e = cudaSuccess;
-    if (!wide_tokens_readable(p)) {
+    if (!wide_tokens_readable(p.x_codes, p.w_codes, p.K)) {
         int8_t *room = static_cast<int8_t *>(p.workspace) + (plan.splits > 1 ? plan.splits * ceil32(p.T) * ceil32(p.N) * 4 : 0);
         wc = {room, pitch16(p.K)};
         xc = {room + copied_bytes(p.N, p.K), pitch16(p.K)};

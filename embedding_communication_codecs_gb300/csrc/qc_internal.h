@@ -380,11 +380,12 @@ cudaError_t launch_join(const JoinParams &p, cudaStream_t stream);
 
 // The product for a batch of tokens, the weights read as codes (qc_int8_wide.cu).
 // wide_tokens_readable(): TMA reads the codes where they lie.
-bool wide_tokens_readable(const ProductParams &p);
-size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K);
+bool wide_tokens_readable(const int8_t *x_codes, const int8_t *w_codes, uint64_t K);
+size_t wide_tokens_workspace(uint64_t T, uint64_t N, uint64_t K, bool readable);
 cudaError_t launch_int8_wide(const ProductParams &p, cudaStream_t stream);
 
-size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K);
+// readable: of the codes, as above.
+size_t int8_matmul_workspace(uint64_t T, uint64_t N, uint64_t K, bool readable);
 size_t int8_input_grad_workspace(uint64_t T, uint64_t N, uint64_t K);
 size_t int8_weight_grad_workspace(uint64_t T, uint64_t N, uint64_t K);
 cudaError_t launch_int8_matmul(const ProductParams &p, cudaStream_t stream);

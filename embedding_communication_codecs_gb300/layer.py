@@ -120,6 +120,11 @@ def qc_int8_matmul_workspace(T, N, K) -> int:
     return int(lib.qc_int8_matmul_workspace(T, N, K))
 
 
+def qc_int8_matmul_codes_workspace(x_codes, w_codes, T, N, K) -> int:
+    """The same for codes where these lie (tensors or addresses)."""
+    return int(lib.qc_int8_matmul_codes_workspace(_ptr(x_codes), _ptr(w_codes), T, N, K))
+
+
 def qc_int8_input_grad_workspace(T, N, K) -> int:
     """Bytes of workspace that qc_int8_input_grad needs."""
     return int(lib.qc_int8_input_grad_workspace(T, N, K))
@@ -353,7 +358,7 @@ def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bf
     N = w_codes.shape[0]
     with _device_of(x_codes=x_codes, x_scale=x_scale, w_codes=w_codes, w_scale=w_scale, bias=bias):
         y = _empty(x_codes, T, N, dtype=dtype)
-        nbytes = lib.qc_int8_matmul_workspace(T, N, K)
+        nbytes = lib.qc_int8_matmul_codes_workspace(x_codes.data_ptr(), w_codes.data_ptr(), T, N, K)
         ws = _scratch(x_codes, nbytes)
         _check(lib.qc_int8_matmul(x_codes.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(), w_scale.data_ptr(), _ptr(bias),
                                   T, N, K, y.data_ptr(), code, N, _ptr(ws), nbytes, _current(x_codes)))
