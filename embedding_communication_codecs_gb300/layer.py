@@ -393,7 +393,8 @@ def int8_weight_grad(dy, x_codes, x_scale, *, dtype=torch.float32, with_bias=Fal
                      stream=None):
     """(dw [N, K], dbias [N] fp32 or None) from dy [T, N] bf16 (dense rows) and the
     codes of x [T, K].  ``into`` = (dw, dbias or None), fp32: the gradients are
-    added to them and they are returned."""
+    added to them and they are returned; ``dtype`` and ``with_bias`` then say nothing and are
+    refused where they contradict it."""
     if stream is not None:
         with _on(stream, dy):
             return int8_weight_grad(dy, x_codes, x_scale, dtype=dtype, with_bias=with_bias, into=into)
@@ -411,7 +412,10 @@ def int8_weight_grad(dy, x_codes, x_scale, *, dtype=torch.float32, with_bias=Fal
     dw = dbias = None
     if into is not None:
         dw, dbias = into
-        dtype = torch.float32
+        if dtype is not torch.float32:
+            raise ValueError(f"into takes fp32 gradients, and dtype is {dtype}")
+        if with_bias and dbias is None:
+            raise ValueError("with_bias, but into holds no dbias")
         _dense(dw, "dw", _F32, (N, K))
         if dbias is not None:
             _dense(dbias, "dbias", _F32, (N,))
