@@ -11,6 +11,9 @@ stream they run on, and return the results.
     y = int8_matmul(x_codes, x_scale, w_codes, w_scale)   # [T, N]
     dx = int8_input_grad(dy, w_codes, w_scale)            # [T, K]
     dw, _ = int8_weight_grad(dy, x_codes, x_scale)        # [N, K], flat for encode_ef
+
+The backward pass is called as it stands here: as elsewhere in this package no call records
+anything for autograd, and results never require a gradient.
 """
 from __future__ import annotations
 
@@ -366,7 +369,11 @@ def int8_matmul(x_codes, x_scale, w_codes, w_scale, bias=None, *, dtype=torch.bf
 
 
 def int8_input_grad(dy, w_codes, w_scale, *, dtype=torch.bfloat16, stream=None):
-    """dx [T, K] from dy [T, N] bf16 (dense rows) and the codes of w [N, K]."""
+    """dx [T, K] from dy [T, N] bf16 (dense rows) and the codes of w [N, K].
+
+    The decoded weights are multiplied as bf16, which is exact under the powers of two of
+    rowwise_int8; under any other w_scale each is rounded once (2^-9), which the forward
+    product, whose scales are applied to its sums, does not do."""
     if stream is not None:
         with _on(stream, dy):
             return int8_input_grad(dy, w_codes, w_scale, dtype=dtype)
@@ -392,7 +399,7 @@ def int8_input_grad(dy, w_codes, w_scale, *, dtype=torch.bfloat16, stream=None):
 def int8_weight_grad(dy, x_codes, x_scale, *, dtype=torch.float32, with_bias=False, into=None,
                      stream=None):
     """(dw [N, K], dbias [N] fp32 or None) from dy [T, N] bf16 (dense rows) and the
-    codes of x [T, K].  ``into`` = (dw, dbias or None), fp32: the gradients are
+    codes of x [T, K]; the decoded x is a bf16, as in int8_input_grad.  ``into`` = (dw, dbias or None), fp32: the gradients are
     added to them and they are returned; ``dtype`` and ``with_bias`` then say nothing and are
     refused where they contradict it."""
     if stream is not None:
