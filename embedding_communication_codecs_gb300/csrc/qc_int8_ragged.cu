@@ -52,7 +52,7 @@ __device__ __forceinline__ typename RawOf<T, 8>::type load8_any(const T *row, in
 // Codes of the elements e .. e + 7, inside the row, at out + e (8-byte aligned).
 __device__ __forceinline__ void store8_any(int8_t *out, int e, int dim, const uint32_t (&c)[8]) {
     if (e >= 0 && e + 8 <= dim) {
-        store_codes<8>(out + e, c);
+        store_codes(out + e, c);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j)

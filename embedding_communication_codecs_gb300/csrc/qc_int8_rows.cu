@@ -6,9 +6,10 @@
 // covers it in units of U consecutive elements, V units per lane at a time.  The
 // encoders read a row once, hold it in registers while the team agrees on the
 // largest magnitude, and write the codes from there; a row that is longer than
-// the largest team holds is read a second time, from L2.  U is 8 (or 16) where
-// rows start on the vector's boundary, so that a lane moves 8 to 32 bytes with one
-// instruction; rows that start anywhere are qc_int8_ragged.cu's.
+// the largest team holds is read a second time, from L2.  U is 8 (4 where fp32 is
+// written), a lane's 8 to 32 bytes, for rows that start on the vector's boundary; rows that
+// start anywhere are qc_int8_ragged.cu's, but for the gated activation's backward pass,
+// which takes them here one element at a time.
 #include <algorithm>
 
 #include "qc_chain.cuh"
@@ -34,7 +35,7 @@ __device__ __noinline__ void encode_rare_row(int8_t *out, uint32_t units, uint32
         uint32_t c[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) c[j] = inverse == 0.0f ? 0u : code_bits(clamp_to_cap(get(u * U + j)), inverse);
-        store_codes<U>(out + u * U, c);
+        store_codes(out + u * U, c);
     }
 }
 

@@ -146,16 +146,9 @@ __device__ __forceinline__ typename RawOf<T, U>::type load_unit(const T *p) {
     return *reinterpret_cast<const typename RawOf<T, U>::type *>(p);
 }
 
-// The codes of U elements, four to a word.
-template <int U>
-__device__ __forceinline__ void store_codes(int8_t *p, const uint32_t (&c)[U]) {
-    if constexpr (U == 1) {
-        *p = static_cast<int8_t>(c[0] & 0xFFu);
-    } else {
-        static_assert(U == 8, "a unit is 8 bytes of codes");
-        *reinterpret_cast<uint2 *>(p) =
-            make_uint2(pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7]));
-    }
+// The codes of eight elements, four to a word.
+__device__ __forceinline__ void store_codes(int8_t *p, const uint32_t (&c)[8]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_codes(c[0], c[1], c[2], c[3]), pack_codes(c[4], c[5], c[6], c[7]));
 }
 
 // U fp32 values rounded to the output's type.
@@ -235,7 +228,7 @@ __device__ __forceinline__ void encode_unit(int8_t *out, float inverse, Get get)
     uint32_t c[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) c[j] = code_bits(get(j), inverse);
-    store_codes<U>(out, c);
+    store_codes(out, c);
 }
 
 // U codes as they lie in memory.  A code becomes a float without a conversion
@@ -253,6 +246,14 @@ struct RawCodes<1> {
     int8_t b;
     __device__ __forceinline__ float get(int) const { return static_cast<float>(b); }
 };
+
+// Four codes -> two f16 pairs: each byte, offset by 128, under the exponent of
+// 2^10 (1024 + 128 + code), minus 1152.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    w ^= 0x80808080u;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
+}
 
 // sigma(g) = 1 / (1 + exp(-g)) and 1 - sigma(g).
 //

@@ -90,14 +90,6 @@ __device__ __forceinline__ WideUnit wide_unit(uint32_t u, const WideParams &P) {
     return {u / tiles_t % tiles_n, u % tiles_t, split, first, min(P.split_steps, all - first)};
 }
 
-// Four codes -> two f16 pairs (each byte, offset by 128, under the exponent of 2^10,
-// minus 1024 + 128).
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    w ^= 0x80808080u;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(__byte_perm(w, 0x64646464u, 0x4140)), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(__byte_perm(w, 0x64646464u, 0x4342)), "r"(0x64806480u));
-}
-
 // scaled_far() of a lane's eight sums, whose tokens' scales lanes `first` on hold.  One call for
 // eight: unrolled into the stores, tiles of 128 tokens took 31.1 us (16384 x 4096) instead of 29.2.
 struct Eight {
@@ -251,10 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     *reinterpret_cast<uint4 *>(at + (((2 * (p & 3) + 1) ^ (t & 7)) << 4)) = hi;
                 }
                 fence_proxy_async_shared();
-                // The stage is given back only here, where its codes have been widened and stored.
-                // Given back right after the loads, before their values were used, it was refilled
-                // under some of them (measured: wrong tokens in tiles of 64); 16384 x 4096
-                // with 64 tokens takes 20 us either way, with 128 30.5 us against 27.8.
+                // The stage is given back only here, where its codes have been widened and stored: the
+                // stores depend on the loaded values, so no load can come later.  Given back
+                // right after the loads, it was refilled under some of them (measured: wrong
+                // tokens in tiles of 64, none with volatile loads).  16384 x 4096 with 128 tokens takes
+                // 29 us, 28 in the other order; with 64 tokens 21 either way.
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
                 tmem_wait_store();
