@@ -64,3 +64,19 @@ def test_scales_that_are_not_finite():
         want = torch.full((T, N), float(K), device="cuda")
         want[T - 1], want[:, 2] = float("nan"), float("nan")
         assert torch.equal(torch.nan_to_num(y, nan=-1.0), torch.nan_to_num(want, nan=-1.0))
+
+
+@pytest.mark.parametrize("T,N,K", SIZES)
+def test_subnormal_scales(T, N, K):
+    """Scales below 2^-126, whole in fp32 whatever the other one is, against large ones."""
+    import embedding_communication_codecs_gb300 as q
+    rng = np.random.default_rng([T, N, K, 1])
+    x = rng.integers(-16, 17, (T, K)).astype(np.int8)
+    w = rng.integers(-16, 17, (N, K)).astype(np.int8)
+    small = (rng.integers(1, 1 << 22, T).astype(np.uint32)).view(np.float32)       # subnormal
+    large = (np.exp2(rng.integers(100, 127, N).astype(np.float64)) * rng.uniform(1, 1.9, N)).astype(np.float32)
+    for sx, sw in ((small, large), (np.resize(large, T), np.resize(small, N))):
+        y = q.int8_matmul(*(torch.from_numpy(a).cuda() for a in (x, sx, w, sw)), dtype=torch.float32).double().cpu().numpy()
+        want = (x.astype(np.float64) @ w.astype(np.float64).T) * sx.astype(np.float64)[:, None] * sw.astype(np.float64)
+        # two roundings of the three fractions, and a subnormal result's own
+        assert (np.abs(y - want) <= 3 * plain.U * np.abs(want) + 2.0 ** -149).all()
